@@ -179,7 +179,7 @@ using namespace gdn2;
 
 extern "C" {
 
-int32_t gdn2_version(void) { return (1 << 16) | 1; }
+int32_t gdn2_version(void) { return (1 << 16) | 2; }
 
 const char *gdn2_status_string(int status) {
     switch (status) {
@@ -199,6 +199,7 @@ const char *gdn2_status_string(int status) {
         case GDN2_ERR_NOALLOC_LIMIT: return "problem needs more scratch than the allocation-free entry point holds (GDN2_NOALLOC_SCRATCH_BYTES)";
         case GDN2_ERR_RANGE: return "a value passed the range of the fp16 intermediates and was clipped (outputs invalid)";
         case GDN2_ERR_BOUNDS: return "an index check of the checked build failed (outputs invalid; a library defect)";
+        case GDN2_ERR_PAGES: return "a cached length, a token's place or a page-table entry is out of range on the device";
         default: return "unknown status";
     }
 }

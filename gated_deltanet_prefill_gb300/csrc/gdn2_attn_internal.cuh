@@ -1,0 +1,64 @@
+// Internal declarations of the attention-layer operators (include/gdn2_attn.h).
+#pragma once
+
+#include "gdn2_attn.h"
+#include "gdn2_internal.cuh"
+
+namespace gdn2 {
+
+// Workspace of the append call: the status words only.
+constexpr size_t kAppendWorkspaceBytes = 64;
+
+// Norm and rotation, with or without the paged cache as the keys' target.
+struct RopeParams {
+    const bf16 *q, *k, *v;              // dtype of the call (the bits are fp16 when f16)
+    const bf16 *q_weight, *k_weight;    // null: ones
+    const double *inv_freq;
+    const void *positions;              // null: the places in the cached sequences
+    int pos64;
+    bf16 *q_out, *k_out;                // k_out: null with the paged cache
+    bf16 *k_cache, *v_cache;
+    int64_t sq_t, sq_h, sk_t, sk_h, sv_t, sv_h, sqo_t, sqo_h, sko_t, sko_h;
+    int64_t skc[3], svc[3];             // page, token in the page, head
+    const void *cu;
+    int cu64;
+    const int *kv_lens, *table;
+    int64_t table_stride;
+    int64_t num_pages;
+    int64_t T;
+    int N, HQ, HK, HV;                  // heads of q, k and v that the call has (0: left out)
+    int page_size, max_pages;
+    int rot_dim, norm;
+    float eps, factor;
+    int *status;                        // null without the paged cache
+};
+
+cudaError_t launch_rope(const RopeParams &p, int D, bool f16, bool interleaved, int sms, cudaStream_t s);
+
+struct AttnParams {
+    const bf16 *q, *k_cache, *v_cache;
+    bf16 *out;
+    float *lse;
+    int64_t sq_t, sq_h, so_t, so_h;
+    int64_t skc[3], svc[3];
+    const void *cu;
+    int cu64;
+    const int *kv_lens, *table;
+    int64_t table_stride;
+    int64_t num_pages;
+    int64_t T;
+    int N, HQ, HKV, G;                  // G = HQ / HKV query heads per key head
+    int page_size, max_pages;
+    int causal, window;                 // window < 0: none
+    float scale;
+    int *status;
+};
+
+size_t paged_attn_workspace(const gdn2_attn_dims &d);
+cudaError_t launch_paged_attn(const AttnParams &p, int D, bool f16, int sms, void *workspace, cudaStream_t s);
+
+__device__ __forceinline__ int64_t cu_of(const void *cu, int cu64, int i) {
+    return cu64 ? static_cast<const int64_t *>(cu)[i] : static_cast<int64_t>(static_cast<const int32_t *>(cu)[i]);
+}
+
+}  // namespace gdn2

@@ -66,9 +66,11 @@ typedef enum gdn2_status {
     GDN2_ERR_RANGE = 14,      /* device-side: a value passed the range of the fp16    */
                               /* intermediates and was clipped; outputs are invalid   */
                               /* (see gdn2_device_status)                             */
-    GDN2_ERR_BOUNDS = 15      /* device-side, checked builds only (compiled with      */
+    GDN2_ERR_BOUNDS = 15,     /* device-side, checked builds only (compiled with      */
                               /* GDN2_CHECK_BOUNDS): an index left its buffer; a      */
                               /* library defect, outputs invalid                      */
+    GDN2_ERR_PAGES = 16       /* device-side (gdn2_attn.h): a cached length, a token's */
+                              /* place or a page-table entry is out of range          */
 } gdn2_status;
 
 typedef enum gdn2_dtype {
