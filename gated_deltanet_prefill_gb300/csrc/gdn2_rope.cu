@@ -1,145 +1,312 @@
 // Per-head RMS norm and rotary position embedding of queries and keys, and the
 // same on the way into a paged key/value cache (include/gdn2_attn.h).
 //
-// One warp per (token, head) row; the row's channels sit in shared memory
-// between the norm and the rotation.
+// Per row x of D channels with weight w, rotated pair (a, b) and angle z:
+//   r = 1 / sqrt(mean(x^2) + eps)
+//   y_a = m r (x_a w_a cos z - x_b w_b sin z),  y_b = m r (x_b w_b cos z + x_a w_a sin z)
+// so every channel is y = r (x A + x_partner B), where A and B hold the weight,
+// the sine or cosine and the factor m, and depend on the token and the channel
+// but not on the head.  A half-warp (D = 128; a quarter for D = 64) holds one
+// row, 8 channels per lane in one 16-byte load; a lane keeps its channels for
+// all heads of its token, so A and B are formed once per token for the queries
+// and once for the keys, and a row costs one load, the shuffles of the sum of
+// squares, those that fetch the partner's 8 channels (half layout; in the
+// interleaved one the partner is in the lane) and 16 multiply-adds.
+//
+// Bound by memory: the bytes in and out are all there is.  A warp takes all
+// heads of a token when there are tokens enough to fill the GPU, and a slice
+// of them otherwise, so that a decode step is one row group per warp.
 #include "gdn2_attn_internal.cuh"
+#include "gdn2_tc.cuh"
 
 namespace gdn2 {
 namespace {
 
-// Angle per position as a fraction of a turn, in units of 2^-64 turns: f
-// radians (f >= 0, finite) times 2^64 / (2 pi), modulo a turn.  position *
-// fraction wraps modulo a turn by itself, so the angle of any position is
-// exact to the frequency's own rounding.
+using namespace tc;
+
+constexpr int kWarps = 4;    // warps per block
+constexpr int kUnroll = 4;   // row groups in flight per warp
+// Resident warps that the slicing aims at, per SM.
+constexpr int kWarpsPerSm = 32;
+
+// Angle per position as a fraction of a turn in units of 2^-64 turns: f / (2
+// pi) * 2^64 modulo 2^64, from the double's bits (integers only: double
+// arithmetic would cost more than the rest of the token).  position * fraction
+// wraps modulo a turn by itself, so the angle of any position is exact to the
+// frequency's own rounding.  With f = M 2^(e - 63), M in [2^63, 2^64), and
+// C = 2^66 / (2 pi): f 2^64 / (2 pi) = M C 2^(e - 65).
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
-    const double t = f * 0.15915494309189533577;
-    return static_cast<uint64_t>((t - floor(t)) * 18446744073709551616.0);
-}
-
-__device__ __forceinline__ float to_f(bf16 x, bool f16) {
-    return f16 ? __half2float(*reinterpret_cast<const __half *>(&x)) : __bfloat162float(x);
-}
-__device__ __forceinline__ void put(bf16 *p, float x, bool f16) {
-    if (f16)
-        *reinterpret_cast<__half *>(p) = __float2half_rn(x);
+    constexpr uint64_t C = 0xA2F9836E4E441529ull;  // floor(2^66 / (2 pi)) = floor(2^64 * 2 / pi)
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+    const int e = static_cast<int>((bits >> 52) & 2047) - 1023;
+    const uint64_t M = (bits << 11) | (1ull << 63);
+    const uint64_t hi = __umul64hi(M, C), lo = M * C;
+    // (hi 2^64 + lo) 2^(e - 65)
+    uint64_t r;
+    if (e <= 1)
+        r = 1 - e < 64 ? hi >> (1 - e) : 0;
+    else if (e <= 64)
+        r = (hi << (e - 1)) | (lo >> (65 - e));
     else
-        *p = __float2bfloat16_rn(x);
+        r = e < 129 ? lo << (e - 65) : 0;
+    return bits >> 63 ? 0 - r : r;
 }
 
-// The sequence of token t (the last n with cu[n] <= t), or -1.
-__device__ int sequence_of(const RopeParams &p, int64_t t) {
-    int lo = 0, hi = p.N;  // cu[lo] <= t < cu[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (cu_of(p.cu, p.cu64, mid) <= t)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return p.N > 0 && cu_of(p.cu, p.cu64, lo) <= t && t < cu_of(p.cu, p.cu64, lo + 1) ? lo : -1;
+// Sine and cosine of position * fraction turns.  The angle is reduced exactly,
+// then one multiply-add rounds it; on [-pi, pi] the special-function unit errs
+// by 2^-21, far below the outputs' 16 bits.
+__device__ __forceinline__ void turn_sincos(int64_t pos, uint64_t fraction, float &s, float &c) {
+    const int32_t a = static_cast<int32_t>((static_cast<uint64_t>(pos) * fraction) >> 32);
+    __sincosf(static_cast<float>(a) * 1.4629180792671596e-9f, &s, &c);  // a 2^-32 turns, 2 pi / 2^32
 }
 
-// Page and slot of a token's place; false if the place or the entry is bad.
-__device__ bool place_of(const RopeParams &p, int64_t t, int64_t &place, int64_t &page, int &slot) {
-    const int n = sequence_of(p, t);
-    if (n < 0) return false;
-    place = p.kv_lens[n] - (cu_of(p.cu, p.cu64, n + 1) - t);
-    if (place < 0 || place / p.page_size >= p.max_pages) return false;
-    page = p.table[n * p.table_stride + place / p.page_size];
-    slot = static_cast<int>(place % p.page_size);
-    return page >= 0 && page < p.num_pages;
+// The sequence of token t, -1 if there is none; all lanes get the same.
+__device__ __forceinline__ int sequence_of(const RopeParams &p, int64_t t, int lane) {
+    int lo = 0, hi = p.N;
+    if (hi <= 0) return -1;
+    do {
+        const int step = (hi - lo + 31) >> 5;
+        const int i = lo + lane * step;
+        const uint32_t below = __ballot_sync(0xffffffffu, i < hi && cu_of(p.cu, p.cu64, i) <= t);
+        if (!below) return -1;
+        lo += (31 - __clz(below)) * step;
+        hi = min(hi, lo + step);
+    } while (hi - lo > 1);
+    return lo;
 }
 
-__global__ void rope_status_kernel(RopeParams p) {
+struct Place {
+    int64_t place, page;
+    int slot;
+    bool ok;
+};
+
+__device__ __forceinline__ Place place_of(const RopeParams &p, int64_t t, int lane) {
+    Place r = {0, 0, 0, false};
+    const int n = sequence_of(p, t, lane);
+    if (n < 0) return r;
+    const int64_t end = cu_of(p.cu, p.cu64, n + 1);
+    r.place = p.kv_lens[n] - (end - t);
+    if (t >= end || r.place < 0 || r.place >= static_cast<int64_t>(p.max_pages) * p.page_size) return r;
+    const int at = static_cast<int>(r.place);
+    const int col = at / p.page_size;
+    r.slot = at - col * p.page_size;
+    r.page = p.table[n * p.table_stride + col];
+    r.ok = r.page >= 0 && r.page < p.num_pages;
+    return r;
+}
+
+// Checks cu_seqlens, the new tokens' places and their table entries, and
+// writes the status words; run by one block (which alone writes them, so that
+// the words need no clearing before the call).
+__device__ void check_tables(const RopeParams &p) {
     __shared__ int bad_cu, bad_page;
-    if (threadIdx.x == 0) {
-        bad_cu = p.N > 0 ? cu_of(p.cu, p.cu64, 0) != 0 || cu_of(p.cu, p.cu64, p.N) != p.T : p.T != 0;
-        bad_page = 0;
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) bad_cu = bad_page = 0;
+    __syncthreads();
+    if (tid == 0 && (p.N > 0 ? cu_of(p.cu, p.cu64, 0) != 0 || cu_of(p.cu, p.cu64, p.N) != p.T : p.T != 0)) bad_cu = 1;
+    auto bad_entry = [&](int n, int col) {
+        const int64_t page = p.table[n * p.table_stride + col];
+        return page < 0 || page >= p.num_pages;
+    };
+    for (int base = tid - lane; base < p.N; base += blockDim.x) {  // 32 sequences per warp
+        const int n = base + lane;
+        int col0 = 0, cols = 0;
+        if (n < p.N) {
+            const int64_t a = cu_of(p.cu, p.cu64, n), b = cu_of(p.cu, p.cu64, n + 1), len = p.kv_lens[n];
+            if (a > b || a < 0 || b > p.T) {
+                bad_cu = 1;
+            } else if (a < b) {
+                if (len < b - a || len > static_cast<int64_t>(p.max_pages) * p.page_size) {
+                    bad_page = 1;
+                } else {
+                    col0 = static_cast<int>((len - (b - a)) / p.page_size);
+                    cols = static_cast<int>((len - 1) / p.page_size) + 1 - col0;
+                }
+            }
+        }
+        if (cols > 0 && bad_entry(n, col0)) bad_page = 1;
+        for (uint32_t more = __ballot_sync(0xffffffffu, cols > 1); more; more &= more - 1) {
+            const int src = __ffs(more) - 1;
+            const int c0 = __shfl_sync(0xffffffffu, col0, src), c = __shfl_sync(0xffffffffu, cols, src);
+            for (int i = 1 + lane; i < c; i += 32)
+                if (bad_entry(base + src, c0 + i)) bad_page = 1;
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.N; i += blockDim.x)
-        if (cu_of(p.cu, p.cu64, i) > cu_of(p.cu, p.cu64, i + 1)) bad_cu = 1;
-    __syncthreads();
-    if (!bad_cu)
-        for (int64_t t = threadIdx.x; t < p.T; t += blockDim.x) {
-            int64_t place, page;
-            int slot;
-            if (!place_of(p, t, place, page, slot)) bad_page = 1;
+    if (tid < 8) p.status[tid] = tid ? 0 : bad_cu ? GDN2_ERR_CU_SEQLENS : bad_page ? GDN2_ERR_PAGES : GDN2_OK;
+}
+
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
+    if (F16)
+        unpack8_f16(u, f);
+    else
+        unpack8_bf(u, f);
+}
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    if (!F16) return pack8_bf(f);
+    return make_uint4(pack_f16_rn(f[0], f[1]), pack_f16_rn(f[2], f[3]), pack_f16_rn(f[4], f[5]),
+                      pack_f16_rn(f[6], f[7]));
+}
+
+// PAGED: keys and values go to their pages, and block 0 checks the tables.
+template <int D, bool F16, bool INTER, bool PAGED>
+__global__ void __launch_bounds__(32 * kWarps) gdn2_rope_kernel(const __grid_constant__ RopeParams p, int slices,
+                                                                int rows_per_slice) {
+    constexpr int L = D / 8;    // lanes per row
+    constexpr int R = 32 / L;   // rows per warp and load
+    if (PAGED && blockIdx.x == 0) {
+        check_tables(p);
+        return;
+    }
+    const int lane = threadIdx.x & 31, c = lane % L, sub = lane / L;
+    const int64_t warp = static_cast<int64_t>(blockIdx.x - (PAGED ? 1 : 0)) * kWarps + (threadIdx.x >> 5);
+    const int64_t t = warp / slices;
+    if (t >= p.T) return;
+    const int r0 = static_cast<int>(warp - t * slices) * rows_per_slice;
+    const int r1 = min(r0 + rows_per_slice, p.HQ + p.HK + p.HV);
+
+    Place at = {0, 0, 0, true};
+    if (PAGED) {
+        at = place_of(p, t, lane);
+        if (!at.ok) return;
+    }
+    const bool turned = 8 * c < p.rot_dim;
+    const int half = p.rot_dim >> 1;
+    const bool second = !INTER && 8 * c >= half;
+    const int partner = INTER || !turned ? c : second ? c - half / 8 : c + half / 8;
+    constexpr int F = INTER ? 4 : 8;
+    float cs[F], sn[F];  // times the factor; the sine signed for this lane's side of the pair
+#pragma unroll
+    for (int e = 0; e < F; ++e) { cs[e] = 1.f; sn[e] = 0.f; }
+    if (turned) {
+        const int64_t pos = PAGED && !p.positions ? at.place
+                            : p.pos64             ? static_cast<const int64_t *>(p.positions)[t]
+                                                  : static_cast<const int32_t *>(p.positions)[t];
+        const double *f = p.inv_freq + (INTER ? 4 * c : second ? 8 * c - half : 8 * c);
+#pragma unroll
+        for (int e = 0; e < F; ++e) {
+            turn_sincos(pos, turn_fraction(f[e]), sn[e], cs[e]);
+            cs[e] *= p.factor;
+            sn[e] *= second || INTER ? p.factor : -p.factor;
         }
-    __syncthreads();
-    if (threadIdx.x < 8)
-        p.status[threadIdx.x] = threadIdx.x ? 0 : bad_cu ? GDN2_ERR_CU_SEQLENS : bad_page ? GDN2_ERR_PAGES : GDN2_OK;
+    }
+
+    // rows [lo, hi) of one kind: queries or keys
+    auto rows = [&](int lo, int hi, const bf16 *x, int64_t sx, bf16 *y, int64_t sy, const bf16 *w) {
+        if (lo >= hi) return;
+        float A[8], B[8];
+        {
+            float wa[8], wb[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.f;
+            if (w) {
+                unpack8<F16>(*reinterpret_cast<const uint4 *>(w + 8 * c), wa);
+                unpack8<F16>(*reinterpret_cast<const uint4 *>(w + 8 * partner), wb);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                A[e] = wa[e] * cs[INTER ? e / 2 : e];
+                B[e] = INTER ? wb[e ^ 1] * (e & 1 ? sn[e / 2] : -sn[e / 2]) : wb[e] * sn[e];
+            }
+        }
+        const int src = lane - c + partner;
+        for (int h0 = lo; h0 < hi; h0 += R * kUnroll) {
+            uint4 u[kUnroll];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const int h = h0 + i * R + sub;
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (h < hi) u[i] = *reinterpret_cast<const uint4 *>(x + h * sx + 8 * c);
+            }
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                if (h0 + i * R >= hi) break;  // the same for all lanes
+                float v[8], o[8];
+                unpack8<F16>(u[i], v);
+                float r = 1.f;
+                if (p.norm) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+#pragma unroll
+                    for (int d = L / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    r = rsqrtf(sum * (1.f / D) + p.eps);
+                }
+                if (INTER) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = r * (v[e] * A[e] + (turned ? v[e ^ 1] * B[e] : 0.f));
+                } else {
+                    uint4 q;
+                    q.x = __shfl_sync(0xffffffffu, u[i].x, src);
+                    q.y = __shfl_sync(0xffffffffu, u[i].y, src);
+                    q.z = __shfl_sync(0xffffffffu, u[i].z, src);
+                    q.w = __shfl_sync(0xffffffffu, u[i].w, src);
+                    float z[8];
+                    unpack8<F16>(q, z);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = r * (v[e] * A[e] + (turned ? z[e] * B[e] : 0.f));
+                }
+                const int h = h0 + i * R + sub;
+                if (h < hi) *reinterpret_cast<uint4 *>(y + h * sy + 8 * c) = pack8<F16>(o);
+            }
+        }
+    };
+    rows(r0, min(r1, p.HQ), p.q + t * p.sq_t, p.sq_h, p.q_out + t * p.sqo_t, p.sqo_h, p.q_weight);
+    const int k0 = p.HQ, v0 = p.HQ + p.HK;
+    rows(max(r0, k0) - k0, min(r1, v0) - k0, p.k + t * p.sk_t, p.sk_h,
+         PAGED ? p.k_cache + at.page * p.skc[0] + at.slot * p.skc[1] : p.k_out + t * p.sko_t,
+         PAGED ? p.skc[2] : p.sko_h, p.k_weight);
+    if (PAGED) {
+        const bf16 *x = p.v + t * p.sv_t;
+        bf16 *y = p.v_cache + at.page * p.svc[0] + at.slot * p.svc[1];
+        const int hi = r1 - v0;
+        for (int h0 = max(r0, v0) - v0 + sub; h0 < hi; h0 += R * kUnroll) {
+            uint4 u[kUnroll];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (h0 + i * R < hi) u[i] = *reinterpret_cast<const uint4 *>(x + (h0 + i * R) * p.sv_h + 8 * c);
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (h0 + i * R < hi) *reinterpret_cast<uint4 *>(y + (h0 + i * R) * p.svc[2] + 8 * c) = u[i];
+        }
+    }
+}
+
+template <int D, bool F16, bool INTER>
+cudaError_t launch(const RopeParams &p, int sms, cudaStream_t s) {
+    constexpr int R = 32 / (D / 8);
+    const int rows = p.HQ + p.HK + p.HV;
+    int64_t slices = 1, per = rows;
+    if (p.T > 0 && rows > 0) {
+        const int64_t want = (static_cast<int64_t>(sms) * kWarpsPerSm + p.T - 1) / p.T;
+        const int64_t most = (rows + R - 1) / R;
+        slices = want < 1 ? 1 : want > most ? most : want;
+        per = ((rows + slices - 1) / slices + R - 1) / R * R;
+        slices = (rows + per - 1) / per;
+    }
+    const int64_t blocks = rows > 0 ? (p.T * slices + kWarps - 1) / kWarps : 0;
+    if (p.status)
+        gdn2_rope_kernel<D, F16, INTER, true><<<static_cast<unsigned>(blocks + 1), 32 * kWarps, 0, s>>>(
+            p, static_cast<int>(slices), static_cast<int>(per));
+    else if (blocks > 0)
+        gdn2_rope_kernel<D, F16, INTER, false><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, s>>>(
+            p, static_cast<int>(slices), static_cast<int>(per));
+    return cudaGetLastError();
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) rope_kernel(RopeParams p, bool f16, bool interleaved) {
-    __shared__ float row[4][D];
-    const int wp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int heads = p.HQ + p.HK + p.HV;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + wp;
-    const int64_t t = r / heads;
-    int h = static_cast<int>(r % heads);
-    if (t >= p.T) return;
-    int64_t place = 0, page = 0;
-    int slot = 0;
-    if (p.status && !place_of(p, t, place, page, slot)) return;
-    const bool is_q = h < p.HQ, is_v = h >= p.HQ + p.HK;
-    h -= is_v ? p.HQ + p.HK : is_q ? 0 : p.HQ;
-    const bf16 *x = is_q ? p.q + t * p.sq_t + h * p.sq_h : is_v ? p.v + t * p.sv_t + h * p.sv_h : p.k + t * p.sk_t + h * p.sk_h;
-    bf16 *y = is_q ? p.q_out + t * p.sqo_t + h * p.sqo_h
-              : is_v ? p.v_cache + page * p.svc[0] + slot * p.svc[1] + h * p.svc[2]
-              : p.k_out ? p.k_out + t * p.sko_t + h * p.sko_h
-                        : p.k_cache + page * p.skc[0] + slot * p.skc[1] + h * p.skc[2];
-    if (is_v) {
-        for (int c = lane; c < D; c += 32) y[c] = x[c];
-        return;
-    }
-    float sum = 0.f;
-    for (int c = lane; c < D; c += 32) {
-        row[wp][c] = to_f(x[c], f16);
-        sum += row[wp][c] * row[wp][c];
-    }
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (p.norm) {
-        const float inv = rsqrtf(sum / D + p.eps);
-        const bf16 *w = is_q ? p.q_weight : p.k_weight;
-        for (int c = lane; c < D; c += 32) row[wp][c] *= inv * (w ? to_f(w[c], f16) : 1.f);
-    }
-    __syncwarp();
-    const int64_t pos = p.rot_dim == 0 ? 0
-                        : !p.positions ? place
-                        : p.pos64      ? static_cast<const int64_t *>(p.positions)[t]
-                                       : static_cast<const int32_t *>(p.positions)[t];
-    for (int c = lane; c < D; c += 32) {
-        float v = row[wp][c];
-        if (c < p.rot_dim) {
-            const int half = p.rot_dim / 2;
-            const int i = interleaved ? c / 2 : c % half;
-            const bool second = interleaved ? c & 1 : c >= half;
-            const int32_t a = static_cast<int32_t>((static_cast<uint64_t>(pos) * turn_fraction(p.inv_freq[i])) >> 32);
-            float sn, cs;
-            sincospif(static_cast<float>(a) * 4.656612873077393e-10f, &sn, &cs);  // a / 2^31 half turns
-            const float u = row[wp][interleaved ? c ^ 1 : second ? c - half : c + half];
-            v = p.factor * (second ? v * cs + u * sn : v * cs - u * sn);
-        }
-        put(y + c, v, f16);
-    }
+cudaError_t launch_d(const RopeParams &p, bool f16, bool interleaved, int sms, cudaStream_t s) {
+    if (f16) return interleaved ? launch<D, true, true>(p, sms, s) : launch<D, true, false>(p, sms, s);
+    return interleaved ? launch<D, false, true>(p, sms, s) : launch<D, false, false>(p, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams &p, int D, bool f16, bool interleaved, int, cudaStream_t s) {
-    if (p.status) rope_status_kernel<<<1, 256, 0, s>>>(p);
-    const int64_t rows = p.T * (p.HQ + p.HK + p.HV);
-    if (rows > 0) {
-        const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-        if (D == 64)
-            rope_kernel<64><<<grid, 128, 0, s>>>(p, f16, interleaved);
-        else
-            rope_kernel<128><<<grid, 128, 0, s>>>(p, f16, interleaved);
-    }
-    return cudaGetLastError();
+cudaError_t launch_rope(const RopeParams &p, int D, bool f16, bool interleaved, int sms, cudaStream_t s) {
+    return D == 64 ? launch_d<64>(p, f16, interleaved, sms, s) : launch_d<128>(p, f16, interleaved, sms, s);
 }
 
 }  // namespace gdn2
