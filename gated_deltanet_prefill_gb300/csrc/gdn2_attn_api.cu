@@ -57,6 +57,11 @@ bool strides_ok(const void *p, const int64_t *s, int n) {
     return true;
 }
 
+// A cache that the kernels read through tensor maps: no broadcast dimension.
+bool mapped_strides_ok(const gdn2_attn_dims &d, const int64_t *s) {
+    return (d.num_pages <= 1 || s[0] > 0) && (d.page_size <= 1 || s[1] > 0) && (d.HKV <= 1 || s[2] > 0);
+}
+
 // Rows of an output do not overlap one another.
 bool rows_apart(const int64_t *s, int64_t n, int heads, int D) {
     if (heads > 1 && s[1] < D) return false;
@@ -101,7 +106,7 @@ gdn2_status check_rope(const gdn2_attn_dims &d) {
 }
 
 bool paged_shape_ok(const gdn2_attn_dims &d) {
-    return check_common(d) == GDN2_OK && d.HKV > 0 && d.num_pages >= 0 && d.num_pages <= 2147483647ll &&
+    return check_common(d) == GDN2_OK && d.HKV > 0 && d.num_pages >= 1 && d.num_pages <= 2147483647ll &&
            d.page_size >= 8 && d.page_size % 8 == 0 && d.page_size <= (1 << 20) && d.max_pages >= 0 &&
            static_cast<int64_t>(d.max_pages) * d.page_size <= 2147483647ll - 65536 && d.table_stride >= d.max_pages;
 }
@@ -241,7 +246,7 @@ gdn2_status gdn2_kv_append(const void *q, const void *k, const void *v, const vo
     if (!paged_shape_ok(d) || (q && d.HQ < 1)) return GDN2_ERR_SHAPE;
     if (!workspace || !cu_seqlens || (d.N > 0 && (!kv_lens || (d.max_pages > 0 && !block_table))) || !q != !q_out)
         return GDN2_ERR_NULL;
-    if (d.T_tot > 0 && (!k || !v || (d.num_pages > 0 && (!k_cache || !v_cache)) || (d.rot_dim > 0 && !inv_freq)))
+    if (d.T_tot > 0 && (!k || !v || !k_cache || !v_cache || (d.rot_dim > 0 && !inv_freq)))
         return GDN2_ERR_NULL;
     if (!strides_ok(q, d.q_stride, 2) || !strides_ok(k, d.k_stride, 2) || !strides_ok(v, d.v_stride, 2) ||
         !strides_ok(q_out, d.qo_stride, 2) || !strides_ok(k_cache, d.kc_stride, 3) ||
@@ -308,9 +313,10 @@ gdn2_status gdn2_paged_attn_fwd(const void *q, const void *k_cache, const void *
     if (!attn_shape_ok(d) || !isfinite(scale)) return GDN2_ERR_SHAPE;
     if (!workspace || !cu_seqlens || (d.N > 0 && (!kv_lens || (d.max_pages > 0 && !block_table))))
         return GDN2_ERR_NULL;
-    if (d.T_tot > 0 && (!q || !out || (d.num_pages > 0 && (!k_cache || !v_cache)))) return GDN2_ERR_NULL;
+    if (d.T_tot > 0 && (!q || !out || !k_cache || !v_cache)) return GDN2_ERR_NULL;
     if (!strides_ok(q, d.q_stride, 2) || !strides_ok(out, d.qo_stride, 2) || !strides_ok(k_cache, d.kc_stride, 3) ||
-        !strides_ok(v_cache, d.vc_stride, 3) || !aligned16(workspace) || reinterpret_cast<uintptr_t>(lse) % 4)
+        !strides_ok(v_cache, d.vc_stride, 3) || !mapped_strides_ok(d, d.kc_stride) || !mapped_strides_ok(d, d.vc_stride) ||
+        !aligned16(workspace) || reinterpret_cast<uintptr_t>(lse) % 4)
         return GDN2_ERR_STRIDE;
     const Rows rq = rows(q, d.T_tot, d.HQ, d.D, d.q_stride), ro = rows(out, d.T_tot, d.HQ, d.D, d.qo_stride);
     const Rows kc = cache_rows(k_cache, d, d.kc_stride), vc = cache_rows(v_cache, d, d.vc_stride);
@@ -353,8 +359,7 @@ gdn2_status gdn2_paged_attn_fwd(const void *q, const void *k_cache, const void *
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(d.D));
     p.status = static_cast<int *>(workspace);
     cudaGetLastError();
-    return launch_paged_attn(p, d.D, d.dtype == GDN2_DTYPE_F16, sm_count(dev), workspace,
-                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_paged_attn(p, d, sm_count(dev), workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GDN2_OK
                : GDN2_ERR_LAUNCH;
 }

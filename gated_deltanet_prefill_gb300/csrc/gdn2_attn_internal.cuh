@@ -55,7 +55,7 @@ struct AttnParams {
 };
 
 size_t paged_attn_workspace(const gdn2_attn_dims &d);
-cudaError_t launch_paged_attn(const AttnParams &p, int D, bool f16, int sms, void *workspace, cudaStream_t s);
+cudaError_t launch_paged_attn(const AttnParams &p, const gdn2_attn_dims &d, int sms, void *workspace, cudaStream_t s);
 
 __device__ __forceinline__ int64_t cu_of(const void *cu, int cu64, int i) {
     return cu64 ? static_cast<const int64_t *>(cu)[i] : static_cast<int64_t>(static_cast<const int32_t *>(cu)[i]);

@@ -49,7 +49,7 @@ extern "C" {
  *   lse              [T_tot, HQ]       fp32, contiguous
  *
  * Supported: D in {64, 128}; rot_dim a multiple of 16 in 0 .. D; page_size a
- * multiple of 8; HQ a multiple of HKV with at most 128 query heads per key
+ * multiple of 8; num_pages >= 1; HQ a multiple of HKV with at most 128 query heads per key
  * head (gdn2_qk_norm_rope takes any two head counts); T_tot < 2^31 - 2^16.
  */
 typedef struct gdn2_attn_dims {
@@ -155,6 +155,7 @@ GDN2_API size_t gdn2_paged_attn_workspace_bytes(const gdn2_attn_dims *dims);
  *   scale   <= 0 means 1/sqrt(D)
  *   lse     may be NULL
  *   out     must not overlap an input
+ *   caches  no zero strides (broadcast pages or heads)
  *
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
  * `dtype` for the product with v.  What the cache holds past kv_len does not

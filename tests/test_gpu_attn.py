@@ -316,6 +316,10 @@ ATTN = [
     ([5, 9], [300, 2], 24, 128, 1, 64, True, -1, BF, "nhd"),
     ([3, 1], [40, 600], 56, 100, 1, 128, True, -1, BF, "nhd"),
     ([20, 1], [256, 129], 72, 40, 8, 128, True, 200, FP, "nhd"),
+    # several items per CTA: many sequences, whole and cut
+    ([1] * 300, [(37 * i) % 400 for i in range(300)], 16, 4, 2, 64, True, -1, BF, "nhd"),
+    ([1, 2, 0] * 60, [(91 * i) % 700 for i in range(180)], 64, 8, 4, 128, True, -1, BF, "hnd"),
+    ([140, 1, 300] * 10, [(57 * i) % 300 for i in range(30)], 32, 8, 8, 128, True, -1, FP, "nhd"),
 ]
 
 
