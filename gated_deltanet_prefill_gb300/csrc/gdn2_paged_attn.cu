@@ -281,7 +281,11 @@ struct Cfg {
     static constexpr int kRing = NT * kQBytes;
     static constexpr int kSmem = kRing + kStages * kStageBytes + 1024;  // + alignment slack
     static constexpr int kMmaWarp = 4 * NT, kTmaWarp = 4 * NT + 1;
-    static constexpr int kThreads = 32 * (4 * NT + 2);
+    static constexpr int kThreads = NT == 2 ? 384 : 192;
+    // NT = 2: three warpgroups of 168 registers at launch, 64512 in all; the two
+    // softmax groups, which hold a row of scores, take 192 and the third keeps
+    // 120 (2 x 128 x 192 + 128 x 120 = 64512)
+    static constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, const int (&c)[4], uint64_t *bar) {
@@ -292,6 +296,40 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, c
         : "memory");
 }
 
+// One thread of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+// Two fp32 values in a 64-bit register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
+
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     gdn2_paged_attn_kernel(const __grid_constant__ KernelParams p) {
@@ -299,7 +337,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     constexpr int NB = D / 64;  // 64-channel blocks of a row
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], tail, q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], tail, q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drain;
     __shared__ uint32_t s_tmem;
     const AttnParams &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
@@ -314,6 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 128);
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 128);
             mbar_init(&p_full[i], 128);
             mbar_init(&o_full[i], 1);
         }
@@ -334,7 +373,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         atomicExch(a.status + 2, static_cast<int>(GDN2_ERR_TIMEOUT));
     };
 
+    auto few_regs = [] {
+        if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    };
     if (wp == C::kTmaWarp) {
+        few_regs();
         // ------------------------------------------- keys and values: TMA
         const int gran = p.granule, per = kTile / gran;     // granules of a tile
         const int batch = 32 / per;                         // tiles whose table entries one load fetches
@@ -424,106 +467,109 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 warp_wait(&full[i % C::kStages], (i / C::kStages) & 1);
         }
     } else if (wp == C::kMmaWarp) {
+        few_regs();
         // ------------------------------------------- tensor cores: one thread
-        if (lane == 0) {
-            constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, false, !F16);
-            constexpr uint32_t kIdO = idesc_f16kind(kTile, D, false, true, !F16);
-            uint32_t taken = 0;                  // stages taken so far
-            uint32_t steps = 0;                  // key tiles done (NT = 1)
-            uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
-            bool ok = true;
-            auto stage = [&](uint32_t i) { return sRing + (i % C::kStages) * C::kStageBytes; };
-            auto wait_stage = [&](uint32_t i) {
-                if (ok) ok = mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1);
-            };
-            auto scores = [&](int x, int buf, uint32_t k) {  // S of tile x = Q_x K^T
-                tc_fence_after();
+        // The warp goes through the steps together and one elected thread issues:
+        // with elect.sync the compiler keeps descriptors and addresses in uniform
+        // registers, and a product of 16 keys costs 23 cycles to issue; under
+        // `lane == 0` it moves them there one by one, 54 cycles, which the 64
+        // cycles that the product takes do not hide once waits come between.
+        constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, false, !F16);
+        constexpr uint32_t kIdO = idesc_f16kind(kTile, D, false, true, !F16);
+        uint32_t taken = 0;                  // stages taken so far
+        uint32_t steps = 0;                  // key tiles done (NT = 1)
+        uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+        bool ok = true;
+        auto stage = [&](uint32_t i) { return sRing + (i % C::kStages) * C::kStageBytes; };
+        auto wait_stage = [&](uint32_t i) { ok = ok && warp_wait(&full[i % C::kStages], (i / C::kStages) & 1); };
+        // S of tile x = Q_x K^T; then the stage is free if `last`
+        auto scores = [&](int x, int buf, uint32_t k, bool last) {
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_f16(tS(buf), desc_kmajor(sQ + x * C::kQBytes, kTile, kk), desc_kmajor(stage(k), kTile, kk),
                             kIdS, kk > 0);
                 mma_commit(&s_full[buf]);
-            };
-            auto output = [&](int x, int buf, uint32_t v, bool first) {  // O_x (+)= P V
-                tc_fence_after();
+                if (last) mma_commit(&empty[k % C::kStages]);
+            }
+            __syncwarp();
+        };
+        // O_x (+)= P V, each half of the keys as soon as its weights are in; then
+        // the stage is free if `last`, and the product is reported on `done`
+        auto output = [&](int x, int buf, uint32_t v, bool first, bool last, uint64_t *done) {
+            ok = ok && warp_wait(&p_half[buf], p_ph[buf]);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
+                for (int kk = 0; kk < kTile / 32; ++kk)
                     mma_f16_ta(tO(x), tS(buf) + 8 * kk, desc_mnmajor(stage(v), kTile, kk), kIdO, kk > 0 || !first);
-            };
-            auto wait_q = [&](int x) {
-                if (ok) ok = mbar_wait(&q_full[x], q_ph[x]);
-                q_ph[x] ^= 1;
-            };
-            auto wait_p = [&](int buf) {
-                if (ok) ok = mbar_wait(&p_full[buf], p_ph[buf]);
-                p_ph[buf] ^= 1;
-            };
-            for (int s = seg0; s < seg1 && ok; ++s) {
-                const Segment g = p.w.seg[s];
-                const int tiles = g.hi - g.lo;
-                if (tiles == 0) continue;
-                if (NT == 2) {
-                    const int nx = g.ntok > p.tt ? 2 : 1;
-                    uint32_t k = taken++;
-                    wait_stage(k);
-                    for (int x = 0; x < nx; ++x) {
-                        wait_q(x);
-                        if (!ok) break;
-                        scores(x, x, k);
-                    }
-                    if (!ok) break;
-                    mma_commit(&empty[k % C::kStages]);
-                    for (int i = 0; i < tiles && ok; ++i) {
-                        const uint32_t v = taken++;
-                        const bool more = i + 1 < tiles;
-                        if (more) k = taken++;
-                        wait_stage(v);
-                        for (int x = 0; x < nx; ++x) {
-                            wait_p(x);
-                            if (!ok) break;
-                            output(x, x, v, i == 0);
-                            if (!more) mma_commit(&o_full[x]);
-                            if (x == nx - 1) mma_commit(&empty[v % C::kStages]);
-                            if (more) {
-                                if (x == 0) wait_stage(k);
-                                if (!ok) break;
-                                scores(x, x, k);
-                                if (x == nx - 1) mma_commit(&empty[k % C::kStages]);
-                            }
-                        }
-                    }
-                } else {
-                    uint32_t k = taken++;
-                    wait_stage(k);
-                    wait_q(0);
-                    if (!ok) break;
-                    scores(0, steps & 1, k);
-                    mma_commit(&empty[k % C::kStages]);
-                    for (int i = 0; i < tiles && ok; ++i, ++steps) {
-                        if (i + 1 < tiles) {
-                            k = taken++;
-                            wait_stage(k);
-                            if (!ok) break;
-                            scores(0, (steps + 1) & 1, k);
-                            mma_commit(&empty[k % C::kStages]);
-                        }
-                        const uint32_t v = taken++;
-                        wait_stage(v);
-                        wait_p(steps & 1);
-                        if (!ok) break;
-                        output(0, steps & 1, v, i == 0);
-                        mma_commit(&empty[v % C::kStages]);
-                        mma_commit(&o_full[steps & 1]);
+            }
+            __syncwarp();
+            ok = warp_wait(&p_full[buf], p_ph[buf]);
+            p_ph[buf] ^= 1;
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = kTile / 32; kk < kTile / 16; ++kk)
+                    mma_f16_ta(tO(x), tS(buf) + 8 * kk, desc_mnmajor(stage(v), kTile, kk), kIdO, 1);
+                if (last) mma_commit(&empty[v % C::kStages]);
+                if (done) mma_commit(done);
+            }
+            __syncwarp();
+        };
+        auto wait_q = [&](int x) {
+            ok = ok && warp_wait(&q_full[x], q_ph[x]);
+            q_ph[x] ^= 1;
+        };
+        for (int s = seg0; s < seg1 && ok; ++s) {
+            const Segment g = p.w.seg[s];
+            const int tiles = g.hi - g.lo;
+            if (tiles == 0) continue;
+            uint32_t k = taken++;
+            wait_stage(k);
+            if (NT == 2) {
+                const int nx = g.ntok > p.tt ? 2 : 1;
+                for (int x = 0; x < nx && ok; ++x) {
+                    wait_q(x);
+                    if (ok) scores(x, x, k, x == nx - 1);
+                }
+                for (int i = 0; i < tiles && ok; ++i) {
+                    const uint32_t v = taken++;
+                    const bool more = i + 1 < tiles;
+                    if (more) k = taken++;
+                    wait_stage(v);
+                    for (int x = 0; x < nx && ok; ++x) {
+                        output(x, x, v, i == 0, x == nx - 1, more ? nullptr : &o_full[x]);
+                        if (more && x == 0) wait_stage(k);
+                        if (more && ok) scores(x, x, k, x == nx - 1);
                     }
                 }
+            } else {
+                wait_q(0);
+                if (ok) scores(0, steps & 1, k, true);
+                for (int i = 0; i < tiles && ok; ++i, ++steps) {
+                    if (i + 1 < tiles) {
+                        k = taken++;
+                        wait_stage(k);
+                        if (ok) scores(0, (steps + 1) & 1, k, true);
+                    }
+                    const uint32_t v = taken++;
+                    wait_stage(v);
+                    output(0, steps & 1, v, i == 0, true, &o_full[steps & 1]);
+                }
             }
-            if (!ok) fail();
-            mma_commit(&drain);  // nothing may run on in Tensor Memory once it is released
-            if (!mbar_wait(&drain, 0)) fail();
         }
+        if (!ok && lane == 0) fail();
+        // nothing may run on in Tensor Memory once it is released
+        if (elect_one()) mma_commit(&drain);
         __syncwarp();
-    } else {
+        if (!warp_wait(&drain, 0) && lane == 0) fail();
+    } else if (wp < 4 * NT) {
         // ------------------------------------------- softmax: a thread per row
+        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         const int x = NT == 2 ? wp >> 2 : 0, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(wp & 3) << 21;  // TMEM lane of the warp's first row
         const uint32_t inv_g = 65536u / a.G + 1;                     // r / G for r < 128
@@ -612,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(u[c >> 5][c & 31]));
+                    for (int c = 0; c < 128; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], u[c >> 5][c & 31], u[c >> 5][(c & 31) + 1]);
                     const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                     if (i == 0) {
                         m = top;
@@ -642,24 +688,31 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m * sl2;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t scale2 = pair(sl2, sl2), base2 = pair(-base, -base);
+                    uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[32];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const int e = 64 * h + 2 * c;
-                            const float y = ex2(fmaf(__uint_as_float(u[e >> 5][e & 31]), sl2, -base));
-                            const float z = ex2(fmaf(__uint_as_float(u[e >> 5][(e & 31) + 1]), sl2, -base));
-                            sum[c & 1] += y;
-                            sum[2 + (c & 1)] += z;
-                            w[c] = F16 ? pack_f16_rn(y, z) : pack_bf2(y, z);
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = unpair(fma2(pair(__uint_as_float(u[c][2 * e]), __uint_as_float(u[c][2 * e + 1])), scale2, base2));
+                            const float a0 = ex2(y.x), a1 = ex2(y.y);
+                            sum2[e & 1] = add2(sum2[e & 1], pair(a0, a1));
+                            w[e] = F16 ? pack_f16_rn(a0, a1) : pack_bf2(a0, a1);
                         }
-                        tmem_st32(tS(buf) + lanes + 32 * h, w);
+                        tmem_st16(tS(buf) + lanes + 16 * c, w);
+                        if (c == 1) {  // the first half of the keys: their product may begin
+                            tmem_st_wait();
+                            tc_fence_before();
+                            mbar_arrive(&p_half[buf]);
+                        }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 t = unpair(add2(sum2[0], sum2[1]));
+                    l += t.x + t.y;
                     tmem_st_wait();
                     tc_fence_before();
+                } else {
+                    mbar_arrive(&p_half[buf]);
                 }
                 mbar_arrive(&p_full[buf]);
             }
@@ -706,6 +759,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         if (!ok) fail();
         cp_async_wait_all();
+    } else {
+        few_regs();
     }
     __syncthreads();
     if (wp == C::kMmaWarp) {
