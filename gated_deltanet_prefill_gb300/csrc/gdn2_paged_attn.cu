@@ -4,30 +4,35 @@
 // Rows.  The query heads that share a key head are packed into the rows of one
 // matrix product: row r of a 128-row tile is token r / G, head r % G of the
 // group (G = HQ / HKV), so that a decode step's G rows share the keys they
-// read.  A CTA holds one tile (few rows per sequence: decode, bound by the
-// keys' and values' bytes) or two (chunks: bound by the tensor cores; the two
-// tiles share the keys and values in shared memory, and one tile's softmax
-// runs while the tensor cores work on the other's).
+// read.  An item is (sequence, key head, up to two row tiles) with its range of
+// 128-key tiles (after the causal and window masks).
 //
-// Work.  An item is (sequence, key head, row tiles) with its range of 128-key
-// tiles (after the causal and window masks).  The items' key tiles, laid end to
-// end, are cut into equal shares, one per CTA (one CTA per SM), wherever the
-// cuts fall: a share is a list of segments (item, key tiles).  An item cut into
-// several segments leaves unnormalised sums and their maxima in the workspace
-// and the combine kernel joins them, in the order of the segments.  So one long
-// sequence, many short ones and any mixture fill the GPU alike, and the result
-// does not depend on timing.
+// Work.  The items' key tiles, laid end to end, are cut into equal shares, one
+// per CTA (one CTA per SM), wherever the cuts fall: a share is a run of segments
+// (item, key tiles).  An item cut into several segments leaves unnormalised sums
+// and their maxima in the workspace, and the combine kernel joins them in the
+// order of the segments.  So one long sequence, many short ones and any mixture
+// fill the GPU alike, and the result does not depend on timing.  Every CTA finds
+// its own share from the lengths (a sum over the sequences), which takes about a
+// microsecond; a separate planning kernel cost 4 to 25.
 //
-//   plan     one block: checks the lengths, cuts the shares, writes segments
-//   main     per segment: S = Q K^T (tcgen05, fp32 in Tensor Memory), softmax
-//            in registers with a running maximum and sum, P back to Tensor
-//            Memory in 16 bits, O += P V (tcgen05, P from Tensor Memory)
-//   combine  joins the items that were cut
+// A CTA (384 threads):
+//   warps 0-3, 4-7  two softmax groups, a thread per row
+//   warp 8          issues the products (tcgen05): S = Q K^T into Tensor Memory
+//                   (fp32), O += P V with P from Tensor Memory (16 bits)
+//   warp 9          walks the share, hands the segments out through a ring in
+//                   shared memory, and loads keys and values by TMA, straight
+//                   from their pages, into a ring of 128-key stages
+// With two row tiles in an item, group x has tile x and both read every stage;
+// with one (decode), group x has every second key tile, with statistics and
+// outputs of its own that are merged at the end of the segment.  Either way one
+// group's softmax runs while the tensor cores work for the other.
 //
-// Keys and values arrive by TMA, straight from their pages, into a ring of
-// 128-key stages; the last tile's value rows past the range are zeroed (the
-// cache may hold anything there, and 0 x NaN is NaN), the keys' scores masked.
+// The last tile's value rows past the range are zeroed in shared memory (the
+// cache may hold anything there, and 0 x NaN is NaN); the keys' scores are masked.
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "gdn2_attn_internal.cuh"
 #include "gdn2_tc.cuh"
@@ -39,38 +44,38 @@ using namespace tc;
 
 constexpr int kMaxCtas = 152;   // shares at most (SMs of a GB300)
 constexpr int kTile = 128;      // rows of a tile, keys of a tile
-constexpr int kPlanThreads = 1024;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kSegRing = 8;     // segments in flight between the warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Registers: three warpgroups of 168 at launch, 64512 in all; the two softmax
+// groups, which hold a row of scores, take 192 and the third keeps 120
+// (2 x 128 x 192 + 128 x 120 = 64512).
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 
-// A share's piece of an item: new tokens j0 .. j0 + ntok of sequence n, key
+// A share's piece of an item: new tokens tok0 .. tok0 + ntok (rows of q), key
 // head h, key tiles lo .. hi; slot of its partial result, -1 if it is whole.
 struct __align__(16) Segment {
-    int n, h, j0, ntok;
-    int lo, hi, slot, end;  // end: keys from `end` on are not attended to
+    int tok0, h, ntok, slot;
+    int lo, hi;
+    int end;    // keys from `end` on are not attended to
+    int place;  // of the first new token in its cached sequence
 };
 // The item whose pieces the combine kernel joins: the first in slot `slot`,
 // then `more` in slots 2 (cta + 1), 2 (cta + 2), ...
 struct __align__(16) Joint {
-    int n, h, j0, ntok;
-    int slot, more, pad0, pad1;
+    int tok0, h, ntok, slot;
+    int more, pad[3];
 };
-struct SeqPlan {
-    long long cost, base, item;  // key tiles per head; first tile, first item
-};
-
-struct PlanPtrs {
-    int *first, *last;           // [kMaxCtas] segment ids of a share
-    Joint *joint;                // [kMaxCtas]
-    SeqPlan *seq;                // [N]
-    Segment *seg;                // [items + kMaxCtas]; segment of item i in share c: i + c
-    float *part_o;               // [2 kMaxCtas][NT * 128][D]
-    float2 *part_ml;             // [2 kMaxCtas][NT * 128] (log2-scaled maximum, sum)
-};
+enum Flag { kBadCu = 1, kBadPages = 2, kTimeout = 4 };
 
 struct KernelParams {
     AttnParams a;
-    PlanPtrs w;
+    int *flags;                  // [kMaxCtas]
+    Joint *joint;                // [kMaxCtas]
+    float *part_o;               // [2 kMaxCtas][256][D]
+    float2 *part_ml;             // [2 kMaxCtas][256] (log2-scaled maximum, sum)
     float scale_log2;
     int tt;                      // tokens per row tile: 128 / G
     int granule;                 // keys per TMA box
@@ -78,35 +83,22 @@ struct KernelParams {
     CUtensorMap tk, tv;
 };
 
-// One row tile per CTA while the sequences have at most one tile of rows on
-// average (decode, short continuations), else two.  Measured at both ends:
-// see the table of cases.
-int row_tiles(const gdn2_attn_dims &d) {
-    return d.T_tot * (d.HQ / d.HKV) <= static_cast<int64_t>(kTile) * d.N ? 1 : 2;
-}
-
 struct Layout {
-    size_t first, last, joint, seq, seg, part_o, part_ml, total;
+    size_t flags, joint, part_ml, part_o, total;
 };
 Layout layout_of(const gdn2_attn_dims &d) {
-    const int G = d.HQ / d.HKV, nt = row_tiles(d);
-    const size_t tokens = static_cast<size_t>(kTile / G) * nt;
-    const size_t items = (static_cast<size_t>(d.T_tot) / tokens + d.N) * d.HKV;
     Layout l;
     size_t off = 256;  // the status words
     auto take = [&](size_t bytes) { const size_t o = off; off += (bytes + 255) & ~static_cast<size_t>(255); return o; };
-    l.first = take(kMaxCtas * 4);
-    l.last = take(kMaxCtas * 4);
+    l.flags = take(kMaxCtas * 4);
     l.joint = take(kMaxCtas * sizeof(Joint));
-    l.seq = take(static_cast<size_t>(d.N) * sizeof(SeqPlan));
-    l.seg = take((items + kMaxCtas) * sizeof(Segment));
-    l.part_ml = take(2ull * kMaxCtas * nt * kTile * sizeof(float2));
-    l.part_o = take(2ull * kMaxCtas * nt * kTile * d.D * sizeof(float));
+    l.part_ml = take(4ull * kMaxCtas * kTile * sizeof(float2));
+    l.part_o = take(4ull * kMaxCtas * kTile * d.D * sizeof(float));
     l.total = off;
     return l;
 }
 
-// ------------------------------------------------------------------- plan
+// ------------------------------------------------------------- the shares
 struct Span {
     int lo, hi, end;  // key tiles, first key past the range
 };
@@ -120,172 +112,208 @@ __device__ __forceinline__ Span key_span(const AttnParams &a, int len, int fresh
     if (s.hi < s.lo) s.hi = s.lo;
     return s;
 }
-
-__device__ __forceinline__ long long div_by(long long x, long long total) {
-    return (x | total) >> 32 ? x / total : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(total));
+// What an item costs: its key tiles, at least 1 (an item without keys writes zeros).
+__device__ __forceinline__ int item_cost(const AttnParams &a, int len, int fresh, int tokens, int m) {
+    const Span s = key_span(a, len, fresh, m * tokens, min(fresh, (m + 1) * tokens));
+    return max(1, s.hi - s.lo);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) gdn2_attn_plan_kernel(const __grid_constant__ KernelParams p, int ctas, int nt) {
-    __shared__ long long s_cost[33], s_item[33];
-    __shared__ int s_bad_cu, s_bad_len;
-    const AttnParams &a = p.a;
+__device__ __forceinline__ long long div_by(long long x, long long y) {
+    return (x | y) >> 32 ? x / y : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
+
+// A sequence as the shares see it; bad lengths count as no new tokens.
+struct Seq {
+    int t0, fresh, len;
+};
+__device__ __forceinline__ Seq seq_at(const AttnParams &a, int n, int *flags) {
+    Seq q = {0, 0, 0};
+    if (n >= a.N) return q;
+    const int64_t c0 = cu_of(a.cu, a.cu64, n), c1 = cu_of(a.cu, a.cu64, n + 1);
+    const int len = a.kv_lens[n];
+    if (c0 > c1 || c0 < 0 || c1 > a.T) {
+        if (flags) *flags |= kBadCu;
+    } else if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page_size) {
+        if (flags) *flags |= kBadPages;
+    } else {
+        q.t0 = static_cast<int>(c0);
+        q.fresh = static_cast<int>(c1 - c0);
+        q.len = len;
+    }
+    return q;
+}
+
+// Cost of the sequence n = base + threadIdx.x per key head; called by whole warps.
+__device__ long long seq_cost(const AttnParams &a, int n, int tokens, int *flags) {
+    const int lane = threadIdx.x & 31;
+    const Seq q = seq_at(a, n, flags);
+    long long cost = q.fresh == 0 ? 0 : q.fresh <= tokens ? item_cost(a, q.len, q.fresh, tokens, 0) : -1;
+    for (uint32_t more = __ballot_sync(0xffffffffu, cost < 0); more; more &= more - 1) {
+        const int src = __ffs(more) - 1;
+        const int len = __shfl_sync(0xffffffffu, q.len, src), fresh = __shfl_sync(0xffffffffu, q.fresh, src);
+        long long sum = 0;
+        for (int m = lane; m * static_cast<int64_t>(tokens) < fresh; m += 32) sum += item_cost(a, len, fresh, tokens, m);
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == src) cost = sum;
+    }
+    return cost;
+}
+
+struct Share {
+    long long begin, left;   // first key tile, key tiles
+    long long total, shares;
+    long long in_seq, cost;  // offset of the first tile in its sequence, the sequence's cost per head
+    int n, flags;            // sequence of the first tile
+};
+
+// The share of this CTA; every thread of the block calls it, s is in shared memory.
+__device__ void find_share(const AttnParams &a, int tokens, Share &s) {
+    __shared__ long long part[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-    const int tokens = p.tt * nt;
-    pdl_trigger();
+    int flags = 0;
     if (tid == 0) {
-        s_bad_len = 0;
-        s_bad_cu = a.N > 0 ? cu_of(a.cu, a.cu64, 0) != 0 || cu_of(a.cu, a.cu64, a.N) != a.T : a.T != 0;
+        s.flags = 0;
+        s.left = 0;
+        if (a.N > 0 ? cu_of(a.cu, a.cu64, 0) != 0 || cu_of(a.cu, a.cu64, a.N) != a.T : a.T != 0) flags = kBadCu;
     }
-    if (tid < kMaxCtas) {
-        p.w.first[tid] = 0;
-        p.w.last[tid] = -1;
-        p.w.joint[tid].more = 0;
+    long long sum = 0, first = 0;
+    for (int base = 0; base < a.N; base += kThreads) {
+        const long long c = seq_cost(a, base + tid, tokens, &flags);
+        if (base == 0) first = c;
+        sum += c;
     }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[wp] = sum;
     __syncthreads();
-
-    // costs of the sequences, and their running sums
-    long long run_cost = 0, run_item = 0;
-    for (int base = 0; base < a.N; base += kPlanThreads) {
-        const int n = base + tid;
-        int len = 0, fresh = 0, tiles = 0;
-        long long cost = 0;
-        if (n < a.N) {
-            const int64_t c0 = cu_of(a.cu, a.cu64, n), c1 = cu_of(a.cu, a.cu64, n + 1);
-            len = a.kv_lens[n];
-            if (c0 > c1 || c0 < 0 || c1 > a.T)
-                s_bad_cu = 1;
-            else
-                fresh = static_cast<int>(c1 - c0);
-            if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page_size) {
-                s_bad_len = 1;
-                fresh = 0;
-            }
-            tiles = (fresh + tokens - 1) / tokens;
-            if (tiles == 1) {
-                const Span s = key_span(a, len, fresh, 0, fresh);
-                cost = max(1, s.hi - s.lo);
-            }
-        }
-        for (uint32_t more = __ballot_sync(0xffffffffu, tiles > 1); more; more &= more - 1) {
-            const int src = __ffs(more) - 1;
-            const int l = __shfl_sync(0xffffffffu, len, src), f = __shfl_sync(0xffffffffu, fresh, src);
-            const int m = __shfl_sync(0xffffffffu, tiles, src);
-            long long sum = 0;
-            for (int i = lane; i < m; i += 32) {
-                const Span s = key_span(a, l, f, i * tokens, min(f, (i + 1) * tokens));
-                sum += max(1, s.hi - s.lo);
-            }
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == src) cost = sum;
-        }
-        // block scan of (cost, tiles)
-        long long ic = cost, it = tiles;
+    if (flags) atomicOr(&s.flags, flags);
+    long long total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) total += part[i];
+    total *= a.HKV;
+    __syncthreads();
+    if (s.flags || total == 0) return;
+    const long long shares = min(total, static_cast<long long>(gridDim.x));
+    if (blockIdx.x >= shares) return;
+    const long long begin = div_by(total * blockIdx.x, shares), end = div_by(total * (blockIdx.x + 1), shares);
+    long long done = 0;  // tiles of the sequences before the round
+    for (int base = 0; base < a.N; base += kThreads) {
+        const long long c = base == 0 ? first : seq_cost(a, base + tid, tokens, nullptr);
+        long long x = c;
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, ic, o), y = __shfl_up_sync(0xffffffffu, it, o);
-            if (lane >= o) { ic += x; it += y; }
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) part[wp] = x;
+        __syncthreads();
+        long long before = done;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < wp) before += part[i];
+            done += part[i];
+        }
+        const long long from = (before + x - c) * a.HKV;
+        if (begin >= from && begin < from + c * a.HKV) {
+            s.begin = begin;
+            s.left = end - begin;
+            s.total = total;
+            s.shares = shares;
+            s.n = base + tid;
+            s.in_seq = begin - from;
+            s.cost = c;
         }
         __syncthreads();
-        if (lane == 31) { s_cost[wp] = ic; s_item[wp] = it; }
-        __syncthreads();
-        if (wp == 0) {
-            long long x = s_cost[lane], y = s_item[lane];
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-                if (lane >= o) { x += u; y += v; }
-            }
-            s_cost[lane] = x;
-            s_item[lane] = y;
-        }
-        __syncthreads();
-        const long long bc = run_cost + (wp ? s_cost[wp - 1] : 0) + ic - cost;
-        const long long bi = run_item + (wp ? s_item[wp - 1] : 0) + it - tiles;
-        if (n < a.N) p.w.seq[n] = {cost, bc * a.HKV, bi * a.HKV};
-        run_cost += s_cost[31];
-        run_item += s_item[31];
-    }
-    __syncthreads();
-    const bool bad = s_bad_cu || s_bad_len;
-    if (tid < 8) a.status[tid] = tid ? 0 : s_bad_cu ? GDN2_ERR_CU_SEQLENS : s_bad_len ? GDN2_ERR_PAGES : GDN2_OK;
-    const long long total = run_cost * a.HKV;
-    if (bad || total == 0) return;
-    const long long shares = total < ctas ? total : ctas;
-
-    // the segments of one item: tiles [o, o + cost) of the whole row of tiles
-    auto emit = [&](int n, int h, int j0, int ntok, const Span &s, long long item, long long o) {
-        const int cost = max(1, s.hi - s.lo);
-        const bool none = s.hi == s.lo;
-        const int c0 = static_cast<int>(div_by((o + 1) * shares - 1, total));
-        const int c1 = static_cast<int>(div_by((o + cost) * shares - 1, total));
-        for (int c = c0; c <= c1; ++c) {
-            const long long b0 = div_by(total * c, shares), b1 = div_by(total * (c + 1), shares);
-            const bool is_first = o <= b0;
-            Segment g;
-            g.n = n; g.h = h; g.j0 = j0; g.ntok = ntok;
-            g.lo = s.lo + static_cast<int>(max(o, b0) - o);
-            g.hi = none ? s.lo : s.lo + static_cast<int>(min(o + cost, b1) - o);
-            g.slot = c0 == c1 ? -1 : 2 * c + (is_first ? 0 : 1);
-            g.end = s.end;
-            const long long id = item + c;
-            p.w.seg[id] = g;
-            if (is_first) p.w.first[c] = static_cast<int>(id);
-            if (o + cost >= b1) p.w.last[c] = static_cast<int>(id);
-            if (c == c0 && c1 > c0) p.w.joint[c] = {n, h, j0, ntok, g.slot, c1 - c0, 0, 0};
-        }
-    };
-    // sequences of one row tile: a thread per (sequence, head)
-    for (long long i = tid; i < static_cast<long long>(a.N) * a.HKV; i += kPlanThreads) {
-        const int n = static_cast<int>(i / a.HKV), h = static_cast<int>(i - static_cast<long long>(n) * a.HKV);
-        const int fresh = static_cast<int>(cu_of(a.cu, a.cu64, n + 1) - cu_of(a.cu, a.cu64, n));
-        if (fresh == 0 || fresh > tokens) continue;
-        const SeqPlan q = p.w.seq[n];
-        emit(n, h, 0, fresh, key_span(a, a.kv_lens[n], fresh, 0, fresh), q.item + h, q.base + h * q.cost);
-    }
-    // longer ones: a warp per head, a lane per tile
-    for (int n = 0; n < a.N; ++n) {
-        const int fresh = static_cast<int>(cu_of(a.cu, a.cu64, n + 1) - cu_of(a.cu, a.cu64, n));
-        if (fresh <= tokens) continue;
-        const int len = a.kv_lens[n], tiles = (fresh + tokens - 1) / tokens;
-        const SeqPlan q = p.w.seq[n];
-        for (int h = wp; h < a.HKV; h += kPlanThreads / 32) {
-            long long at = q.base + h * q.cost;
-            for (int m0 = 0; m0 < tiles; m0 += 32) {
-                const int m = m0 + lane, j0 = m * tokens;
-                Span s = {0, 0, 0};
-                int cost = 0;
-                if (m < tiles) {
-                    s = key_span(a, len, fresh, j0, min(fresh, j0 + tokens));
-                    cost = max(1, s.hi - s.lo);
-                }
-                int sum = cost;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += x;
-                }
-                if (m < tiles)
-                    emit(n, h, j0, min(tokens, fresh - j0), s, q.item + static_cast<long long>(h) * tiles + m,
-                         at + sum - cost);
-                at += __shfl_sync(0xffffffffu, sum, 31);
-            }
-        }
+        if (done * a.HKV > begin) break;
     }
 }
+
+// The segments of a share, one after the other; a warp walks together.
+struct Walk {
+    const AttnParams &a;
+    int tokens;
+    int n, h, m, off;       // item, key tiles of it already given out
+    int items;              // row-tile groups of the sequence
+    long long left;
+    bool first;
+    Seq q, ahead;           // this sequence, and the next one's loaded ahead
+
+    __device__ void enter() { items = (q.fresh + tokens - 1) / tokens; }
+    __device__ Walk(const AttnParams &a_, int tokens_, const Share &s) : a(a_), tokens(tokens_) {
+        left = s.left;
+        first = true;
+        h = m = off = items = n = 0;
+        q = ahead = {0, 0, 0};
+        if (left <= 0) return;
+        n = s.n;
+        q = seq_at(a, n, nullptr);
+        ahead = seq_at(a, n + 1, nullptr);
+        enter();
+        h = static_cast<int>(div_by(s.in_seq, s.cost));
+        long long at = s.in_seq - h * s.cost;
+        // the item that holds tile `at` of the head
+        const int lane = threadIdx.x & 31;
+        for (;; m += 32) {
+            const int cost = m + lane < items ? item_cost(a, q.len, q.fresh, tokens, m + lane) : 0;
+            int sum = cost;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += x;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, sum > at);
+            if (past || m + 32 >= items) {
+                const int k = past ? __ffs(past) - 1 : 0;
+                at -= __shfl_sync(0xffffffffu, sum - cost, k);
+                m += k;
+                break;
+            }
+            at -= __shfl_sync(0xffffffffu, sum, 31);
+        }
+        off = static_cast<int>(at);
+    }
+    // The next segment; false at the end.  `cut`: it ends before its item does,
+    // by `rest` key tiles.
+    __device__ bool next(Segment &g, int &rest, int &seq) {
+        rest = 0;
+        if (left <= 0) return false;
+        const int j0 = m * tokens;
+        const Span s = key_span(a, q.len, q.fresh, j0, min(q.fresh, j0 + tokens));
+        const int cost = max(1, s.hi - s.lo);
+        const int take = static_cast<int>(min(static_cast<long long>(cost - off), left));
+        seq = n;
+        g.tok0 = q.t0 + j0;
+        g.h = h;
+        g.ntok = min(tokens, q.fresh - j0);
+        g.slot = off > 0 || take < cost ? 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1) : -1;
+        g.lo = s.lo + off;
+        g.hi = s.hi == s.lo ? g.lo : g.lo + take;
+        g.end = s.end;
+        g.place = q.len - q.fresh + j0;
+        rest = cost - off - take;
+        if (off > 0) rest = -rest;  // only the piece that begins the item reports the cut
+        left -= take;
+        first = false;
+        off = 0;
+        if (++m == items) {
+            m = 0;
+            if (++h == a.HKV) {
+                h = 0;
+                do {
+                    ++n;
+                    q = ahead;
+                    ahead = seq_at(a, n + 1, nullptr);
+                } while (q.fresh == 0 && n < a.N);
+                enter();
+            }
+        }
+        return true;
+    }
+};
 
 // ------------------------------------------------------------------- main
-template <int D, int NT>
+template <int D>
 struct Cfg {
     static constexpr int kStageBytes = kTile * D * 2;
     static constexpr int kQBytes = kTile * D * 2;
-    // as many stages as fit beside the query tiles
-    static constexpr int kStages = D == 128 ? (NT == 2 ? 5 : 6) : (NT == 2 ? 10 : 12);
-    static constexpr int kQ = 0;
-    static constexpr int kRing = NT * kQBytes;
+    static constexpr int kStages = D == 128 ? 5 : 10;  // what fits beside the query tiles
+    static constexpr int kRing = 2 * kQBytes;
     static constexpr int kSmem = kRing + kStages * kStageBytes + 1024;  // + alignment slack
-    static constexpr int kMmaWarp = 4 * NT, kTmaWarp = 4 * NT + 1;
-    static constexpr int kThreads = NT == 2 ? 384 : 192;
-    // NT = 2: three warpgroups of 168 registers at launch, 64512 in all; the two
-    // softmax groups, which hold a row of scores, take 192 and the third keeps
-    // 120 (2 x 128 x 192 + 128 x 120 = 64512)
-    static constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, const int (&c)[4], uint64_t *bar) {
@@ -301,6 +329,32 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
     return r != 0;
+}
+
+// Shared-memory descriptors as two words: the low one (address, leading-dimension
+// offset) changes by a constant from step to step, the high one (stride of the
+// 8-row groups, version, 128-byte swizzle) never does.  Building them from a
+// base per stage keeps the issuing thread's work per product to an addition.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4) << 16; }
+// products of 16 keys or channels (see mma_f16, mma_f16_ta)
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 a, b;\n"
+        "mov.b64 a, {%1, %4};\nmov.b64 b, {%2, %4};\n"
+        "setp.ne.b32 p, %5, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 b;\n"
+        "mov.b64 b, {%2, %4};\n"
+        "setp.ne.b32 p, %5, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(acc)
+        : "memory");
 }
 
 // Two fp32 values in a 64-bit register pair, and the packed operations on them.
@@ -330,14 +384,20 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
     return r;
 }
 
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
-    gdn2_paged_attn_kernel(const __grid_constant__ KernelParams p) {
-    using C = Cfg<D, NT>;
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __grid_constant__ KernelParams p) {
+    using C = Cfg<D>;
     constexpr int NB = D / 64;  // 64-channel blocks of a row
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], tail, q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drain;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], tail, drain;
+    __shared__ uint64_t seg_full[kSegRing], seg_empty[kSegRing];
+    // of row tile (q_full) or stream (the others) x
+    __shared__ uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
+    __shared__ uint64_t ml_full, o_free;  // one row tile: group 1's statistics are in; group 0 has read the outputs
+    __shared__ Segment s_seg[kSegRing];
+    __shared__ float2 s_ml[kTile];
+    __shared__ Share s_share;
     __shared__ uint32_t s_tmem;
     const AttnParams &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
@@ -347,73 +407,119 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
+        for (int i = 0; i < kSegRing; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], 9);  // 8 softmax warps and the issuing one
+        }
         mbar_init(&tail, 1);
         mbar_init(&drain, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 128);
+            mbar_init(&q_full[i], 4);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_half[i], 128);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&p_half[i], 4);
+            mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
         }
+        mbar_init(&ml_full, 4);
+        mbar_init(&o_free, 4);
         fence_mbar_init();
     }
-    if (wp == C::kMmaWarp) tmem_alloc(&s_tmem, 512);
+    if (wp == kMmaWarp) tmem_alloc(&s_tmem, 512);
+    pdl_trigger();
+    find_share(a, 2 * p.tt, s_share);
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s_tmem;
-    pdl_trigger();
-    pdl_wait();  // the plan is complete
-    const int seg0 = p.w.first[blockIdx.x], seg1 = p.w.last[blockIdx.x] + 1;
-    const uint32_t sQ = smem_u32(smem + C::kQ), sRing = smem_u32(smem + C::kRing);
-    // Tensor Memory columns: scores of tile (or buffer) x at 128 x, outputs after them
+    const uint32_t sQ = smem_u32(smem), sRing = smem_u32(smem + C::kRing);
+    // Tensor Memory columns: scores of stream x at 128 x, its outputs after them
     auto tS = [&](int x) { return tm + 128 * x; };
     auto tO = [&](int x) { return tm + 256 + 128 * x; };
-    auto fail = [&]() {
-        atomicExch(a.status + 2, static_cast<int>(GDN2_ERR_TIMEOUT));
+    auto fail = [&]() { atomicOr(&s_share.flags, kTimeout); };
+    auto few_regs = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); };
+    // the i-th segment of the share; its last reader in a warp releases it
+    auto seg_wait = [&](uint32_t i) { return warp_wait(&seg_full[i % kSegRing], (i / kSegRing) & 1); };
+    auto seg_done = [&](uint32_t i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[i % kSegRing]);
     };
 
-    auto few_regs = [] {
-        if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    };
-    if (wp == C::kTmaWarp) {
+    if (wp == kTmaWarp) {
+        // ----------------------------- segments; keys and values by TMA
         few_regs();
-        // ------------------------------------------- keys and values: TMA
         const int gran = p.granule, per = kTile / gran;     // granules of a tile
         const int batch = 32 / per;                         // tiles whose table entries one load fetches
         const int my_gr = lane / NB, my_cb = lane % NB;     // this lane's granule and channel block
         uint32_t loads = 0;                                 // tiles loaded so far
+        uint32_t pushed = 0;                                // segments handed out
         int tail_ph = 0;
         bool ok = true;
-        for (int s = seg0; s < seg1 && ok; ++s) {
-            const Segment g = p.w.seg[s];
-            const int tiles = g.hi - g.lo;
-            if (tiles == 0) continue;
-            const int *row = a.table + static_cast<int64_t>(g.n) * a.table_stride;
+        Joint joint = {};
+        Walk walk(a, 2 * p.tt, s_share);
+        // The next segment that has keys, handed out; the others' rows are
+        // written here.  tok0 = -1 ends the share.
+        Segment g;
+        int seq;
+        auto hand_out = [&]() {
+            for (;;) {
+                int rest;
+                if (!walk.next(g, rest, seq)) {
+                    g.tok0 = -1;
+                    break;
+                }
+                if (rest > 0) {
+                    // the item goes on in the shares that its last tile reaches
+                    joint = {g.tok0, g.h, g.ntok, g.slot, 0, {0, 0, 0}};
+                    const long long last = s_share.begin + s_share.left + rest - 1;
+                    joint.more = static_cast<int>(div_by((last + 1) * s_share.shares - 1, s_share.total)) - static_cast<int>(blockIdx.x);
+                }
+                if (g.hi > g.lo) break;
+                for (int i = lane; i < g.ntok * a.G; i += 32) {
+                    const int64_t tok = g.tok0 + i / a.G;
+                    const int head = g.h * a.G + i % a.G;
+                    bf16 *o = a.out + tok * a.so_t + head * a.so_h;
+                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(o + c) = make_uint4(0, 0, 0, 0);
+                    if (a.lse) a.lse[tok * a.HQ + head] = -INFINITY;
+                }
+            }
+            ok = warp_wait(&seg_empty[pushed % kSegRing], ((pushed / kSegRing) & 1) ^ 1);
+            if (!ok) return;
+            if (lane == 0) {
+                s_seg[pushed % kSegRing] = g;
+                mbar_arrive(&seg_full[pushed % kSegRing]);
+            }
+            __syncwarp();
+            ++pushed;
+        };
+        hand_out();
+        while (ok && g.tok0 >= 0) {
+            const Segment cur = g;
+            const int tiles = cur.hi - cur.lo;
+            const int *row = a.table + static_cast<int64_t>(seq) * a.table_stride;
             // page and slot of this lane's granule of the batch that starts at tile t
             auto fetch = [&](int t) {
                 t += lane / per;
                 int2 e = make_int2(0, 0);
                 const int64_t key = static_cast<int64_t>(t) * kTile + (lane % per) * gran;
-                if (t < g.hi && key < g.end) {
+                if (t < cur.hi && key < cur.end) {
                     const int col = static_cast<int>(key) / a.page_size;
                     e = make_int2(row[col], static_cast<int>(key) - col * a.page_size);
                     if (e.x < 0 || e.x >= a.num_pages) {
                         e.x = static_cast<int>(a.num_pages);  // past the tensor: the box reads zeros
-                        atomicCAS(a.status, 0, static_cast<int>(GDN2_ERR_PAGES));
+                        atomicOr(&s_share.flags, kBadPages);
                     }
                 }
                 return e;
             };
             // entries of the batch that the values are in, and of the next
             int at = 0;
-            int2 now = fetch(g.lo), next = fetch(g.lo + batch);
-            // keys or values of tile g.lo + i into the next stage
+            int2 now = fetch(cur.lo), next = fetch(cur.lo + batch);
+            hand_out();  // one segment ahead, so that its queries can be loaded early
+            // keys or values of tile lo + i into the next stage
             auto load = [&](int i, bool is_v) {
                 const int st = static_cast<int>(loads % C::kStages);
-                const int left = min(kTile, g.end - (g.lo + i) * kTile);  // rows that count
+                const int left = min(kTile, cur.end - (cur.lo + i) * kTile);  // rows that count
                 const int grans = (left + gran - 1) / gran;
-                ok = warp_wait(&empty[st], ((loads / C::kStages) & 1) ^ 1);
+                ok = ok && warp_wait(&empty[st], ((loads / C::kStages) & 1) ^ 1);
                 if (!ok) return;
                 const bool patch = is_v && left < kTile;
                 uint64_t *bar = patch ? &tail : &full[st];
@@ -427,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     const int *pos = is_v ? p.vpos : p.kpos;
                     int c[4] = {my_cb * 64, 0, 0, 0};
 #pragma unroll
-                    for (int k = 1; k < 4; ++k) c[k] = pos[0] == k ? page : pos[1] == k ? slot : g.h;
+                    for (int k = 1; k < 4; ++k) c[k] = pos[0] == k ? page : pos[1] == k ? slot : cur.h;
                     tma_load_4d(dst + my_cb * (kTile * 128) + my_gr * gran * 128, is_v ? &p.tv : &p.tk, c, bar);
                 }
                 ++loads;
@@ -446,119 +552,138 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 }
                 if (is_v && (i + 1) % batch == 0) {
                     now = next;
-                    next = fetch(g.lo + (++at + 1) * batch);
+                    next = fetch(cur.lo + (++at + 1) * batch);
                 }
             };
             // in the order in which the products take them: with one row tile
-            // the keys run one tile ahead of the values
-            if (NT == 1) load(0, false);
-            for (int i = 0; i < tiles && ok; ++i) {
-                if (NT == 2)
+            // the keys run two tiles ahead of the values
+            if (cur.ntok > p.tt) {
+                for (int i = 0; i < tiles && ok; ++i) {
                     load(i, false);
-                else if (i + 1 < tiles)
-                    load(i + 1, false);
-                if (ok) load(i, true);
+                    load(i, true);
+                }
+            } else {
+                load(0, false);
+                if (tiles > 1) load(1, false);
+                for (int i = 0; i < tiles && ok; ++i) {
+                    load(i, true);
+                    if (i + 2 < tiles) load(i + 2, false);
+                }
             }
         }
+        if (lane == 0) p.joint[blockIdx.x] = joint;
         if (!ok) {
             if (lane == 0) fail();
             // let the copies in flight land before the block ends
             for (uint32_t i = loads > C::kStages ? loads - C::kStages : 0; i < loads; ++i)
                 warp_wait(&full[i % C::kStages], (i / C::kStages) & 1);
         }
-    } else if (wp == C::kMmaWarp) {
-        few_regs();
+    } else if (wp == kMmaWarp) {
         // ------------------------------------------- tensor cores: one thread
         // The warp goes through the steps together and one elected thread issues:
         // with elect.sync the compiler keeps descriptors and addresses in uniform
         // registers, and a product of 16 keys costs 23 cycles to issue; under
         // `lane == 0` it moves them there one by one, 54 cycles, which the 64
         // cycles that the product takes do not hide once waits come between.
+        few_regs();
         constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, false, !F16);
         constexpr uint32_t kIdO = idesc_f16kind(kTile, D, false, true, !F16);
         uint32_t taken = 0;                  // stages taken so far
-        uint32_t steps = 0;                  // key tiles done (NT = 1)
         uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
         bool ok = true;
+        const uint32_t dq = desc_lo(sQ, 16);
         auto stage = [&](uint32_t i) { return sRing + (i % C::kStages) * C::kStageBytes; };
         auto wait_stage = [&](uint32_t i) { ok = ok && warp_wait(&full[i % C::kStages], (i / C::kStages) & 1); };
-        // S of tile x = Q_x K^T; then the stage is free if `last`
-        auto scores = [&](int x, int buf, uint32_t k, bool last) {
+        // S of stream x = Q K^T with row tile t; then the stage is free if `last`
+        auto scores = [&](int x, int t, uint32_t k, bool last) {
+            if (!ok) return;
             tc_fence_after();
+            const uint32_t dk = desc_lo(stage(k), 16);
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_f16(tS(buf), desc_kmajor(sQ + x * C::kQBytes, kTile, kk), desc_kmajor(stage(k), kTile, kk),
-                            kIdS, kk > 0);
-                mma_commit(&s_full[buf]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    constexpr uint32_t kBlock = kTile * 128 / 16;  // 64 channels of a tile
+                    const uint32_t step = (kk >> 2) * kBlock + (kk & 3) * 2;
+                    mma_ss(tS(x), dq + t * (C::kQBytes / 16) + step, dk + step, kIdS, kk > 0);
+                }
+                mma_commit(&s_full[x]);
                 if (last) mma_commit(&empty[k % C::kStages]);
             }
             __syncwarp();
         };
-        // O_x (+)= P V, each half of the keys as soon as its weights are in; then
-        // the stage is free if `last`, and the product is reported on `done`
-        auto output = [&](int x, int buf, uint32_t v, bool first, bool last, uint64_t *done) {
-            ok = ok && warp_wait(&p_half[buf], p_ph[buf]);
+        // O of stream x (+)= P V, each half of the keys as soon as its weights are
+        // in; then the stage is free if `free`, and the outputs complete if `done`
+        auto output = [&](int x, uint32_t v, bool first, bool free, bool done) {
+            const uint32_t dv = desc_lo(stage(v), kTile * 128);
+            ok = ok && warp_wait(&p_half[x], p_ph[x]);
             if (!ok) return;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
-                    mma_f16_ta(tO(x), tS(buf) + 8 * kk, desc_mnmajor(stage(v), kTile, kk), kIdO, kk > 0 || !first);
+                    mma_ts(tO(x), tS(x) + 8 * kk, dv + 128 * kk, kIdO, kk > 0 || !first);
             }
             __syncwarp();
-            ok = warp_wait(&p_full[buf], p_ph[buf]);
-            p_ph[buf] ^= 1;
+            ok = warp_wait(&p_full[x], p_ph[x]);
+            p_ph[x] ^= 1;
             if (!ok) return;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int kk = kTile / 32; kk < kTile / 16; ++kk)
-                    mma_f16_ta(tO(x), tS(buf) + 8 * kk, desc_mnmajor(stage(v), kTile, kk), kIdO, 1);
-                if (last) mma_commit(&empty[v % C::kStages]);
-                if (done) mma_commit(done);
+                    mma_ts(tO(x), tS(x) + 8 * kk, dv + 128 * kk, kIdO, 1);
+                if (free) mma_commit(&empty[v % C::kStages]);
+                if (done) mma_commit(&o_full[x]);
             }
             __syncwarp();
         };
-        auto wait_q = [&](int x) {
-            ok = ok && warp_wait(&q_full[x], q_ph[x]);
-            q_ph[x] ^= 1;
+        auto wait_q = [&](int t) {
+            ok = ok && warp_wait(&q_full[t], q_ph[t]);
+            q_ph[t] ^= 1;
         };
-        for (int s = seg0; s < seg1 && ok; ++s) {
-            const Segment g = p.w.seg[s];
+        for (uint32_t s = 0; ok; ++s) {
+            ok = seg_wait(s);
+            if (!ok) break;
+            const Segment &g = s_seg[s % kSegRing];
+            if (g.tok0 < 0) break;
             const int tiles = g.hi - g.lo;
-            if (tiles == 0) continue;
+            const bool two = g.ntok > p.tt;
+            seg_done(s);
             uint32_t k = taken++;
             wait_stage(k);
-            if (NT == 2) {
-                const int nx = g.ntok > p.tt ? 2 : 1;
-                for (int x = 0; x < nx && ok; ++x) {
-                    wait_q(x);
-                    if (ok) scores(x, x, k, x == nx - 1);
-                }
+            wait_q(0);
+            scores(0, 0, k, !two);
+            if (two) {
+                wait_q(1);
+                scores(1, 1, k, true);
                 for (int i = 0; i < tiles && ok; ++i) {
                     const uint32_t v = taken++;
                     const bool more = i + 1 < tiles;
                     if (more) k = taken++;
                     wait_stage(v);
-                    for (int x = 0; x < nx && ok; ++x) {
-                        output(x, x, v, i == 0, x == nx - 1, more ? nullptr : &o_full[x]);
-                        if (more && x == 0) wait_stage(k);
-                        if (more && ok) scores(x, x, k, x == nx - 1);
+                    output(0, v, i == 0, false, !more);
+                    if (more) {
+                        wait_stage(k);
+                        scores(0, 0, k, false);
                     }
+                    output(1, v, i == 0, true, !more);
+                    if (more) scores(1, 1, k, true);
                 }
             } else {
-                wait_q(0);
-                if (ok) scores(0, steps & 1, k, true);
-                for (int i = 0; i < tiles && ok; ++i, ++steps) {
-                    if (i + 1 < tiles) {
-                        k = taken++;
-                        wait_stage(k);
-                        if (ok) scores(0, (steps + 1) & 1, k, true);
-                    }
+                if (tiles > 1) {
+                    k = taken++;
+                    wait_stage(k);
+                    scores(1, 0, k, true);
+                }
+                for (int i = 0; i < tiles && ok; ++i) {
                     const uint32_t v = taken++;
                     wait_stage(v);
-                    output(0, steps & 1, v, i == 0, true, &o_full[steps & 1]);
+                    output(i & 1, v, i < 2, true, i + 2 >= tiles);
+                    if (i + 2 < tiles) {
+                        k = taken++;
+                        wait_stage(k);
+                        scores(i & 1, 0, k, true);
+                    }
                 }
             }
         }
@@ -567,100 +692,106 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (elect_one()) mma_commit(&drain);
         __syncwarp();
         if (!warp_wait(&drain, 0) && lane == 0) fail();
-    } else if (wp < 4 * NT) {
+    } else if (wp < 8) {
         // ------------------------------------------- softmax: a thread per row
-        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
-        const int x = NT == 2 ? wp >> 2 : 0, row = tid & 127;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int x = wp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(wp & 3) << 21;  // TMEM lane of the warp's first row
         const uint32_t inv_g = 65536u / a.G + 1;                     // r / G for r < 128
         const float sl2 = p.scale_log2, slack = 8.f / sl2;
         const int my_tok = static_cast<int>((row * inv_g) >> 16), my_head = row - my_tok * a.G;
-        // the row's token of a segment, -1 if it has none
-        auto token = [&](const Segment &g) { return my_tok < p.tt && x * p.tt + my_tok < g.ntok ? x * p.tt + my_tok : -1; };
-        auto next_seg = [&](int s) {  // the next segment with work for this tile
-            while (s < seg1 && (p.w.seg[s].hi == p.w.seg[s].lo || p.w.seg[s].ntok <= x * p.tt)) ++s;
-            return s;
+        // A group signals with one arrival per warp: 128 arrivals on one barrier
+        // take their turns, which the products waited for.
+        auto arrive = [&](uint64_t *bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
         };
-        auto load_q = [&](const Segment &g) {
-            const int rows = min(p.tt, g.ntok - x * p.tt) * a.G;
-            const bf16 *q = a.q + (cu_of(a.cu, a.cu64, g.n) + g.j0 + x * p.tt) * a.sq_t + static_cast<int64_t>(g.h) * a.G * a.sq_h;
-#pragma unroll
+        // queries of row tile t of a segment, by this group
+        auto load_q = [&](const Segment &g, int t) {
+            const int rows = min(p.tt, g.ntok - t * p.tt) * a.G;
+            const bf16 *q = a.q + (static_cast<int64_t>(g.tok0) + t * p.tt) * a.sq_t + static_cast<int64_t>(g.h) * a.G * a.sq_h;
+#pragma unroll 1
             for (int i = 0; i < D / 8; ++i) {
                 const int at = row + 128 * i, r = at / (D / 8), ch = at % (D / 8);
                 const int tok = static_cast<int>((r * inv_g) >> 16), hd = r - tok * a.G;
                 const bool in = r < rows;
-                cp_async16(smem + C::kQ + x * C::kQBytes + (ch >> 3) * (kTile * 128) + swz(r, ch & 7),
+                cp_async16(smem + t * C::kQBytes + (ch >> 3) * (kTile * 128) + swz(r, ch & 7),
                            in ? q + tok * a.sq_t + hd * a.sq_h + 8 * ch : a.q, in ? 16 : 0);
             }
         };
-        auto q_ready = [&]() {
+        auto q_ready = [&](bool t0, bool t1) {
+            if (!t0 && !t1) return;
             cp_async_wait_all();
             fence_proxy_async();
-            mbar_arrive(&q_full[x]);
+            if (t0) arrive(&q_full[0]);
+            if (t1) arrive(&q_full[1]);
         };
-        auto out_row = [&](const Segment &g, int tok) {
-            return a.out + (cu_of(a.cu, a.cu64, g.n) + g.j0 + tok) * a.so_t + static_cast<int64_t>(g.h * a.G + my_head) * a.so_h;
-        };
-        auto put_lse = [&](const Segment &g, int tok, float v) {
-            if (a.lse) a.lse[(cu_of(a.cu, a.cu64, g.n) + g.j0 + tok) * a.HQ + g.h * a.G + my_head] = v;
-        };
-        // items without a key
-        for (int s = seg0; s < seg1; ++s) {
-            const Segment g = p.w.seg[s];
-            if (g.hi > g.lo) continue;
-            const int tok = token(g);
-            if (tok < 0) continue;
-            bf16 *o = out_row(g, tok);
-            for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(o + c) = make_uint4(0, 0, 0, 0);
-            put_lse(g, tok, -INFINITY);
+        bool ok = seg_wait(0);
+        uint32_t steps = 0;              // tiles of this stream so far
+        uint32_t o_ph[2] = {0, 0};       // segments in which stream 0, 1 had tiles
+        uint32_t merges = 0;             // segments that were merged
+        if (ok && s_seg[0].tok0 >= 0) {
+            const bool t1 = x == 1 && s_seg[0].ntok > p.tt;
+            if (x == 0) load_q(s_seg[0], 0);
+            if (t1) load_q(s_seg[0], 1);
+            q_ready(x == 0, t1);
         }
-        // NT = 1: the product of step i is in.  Its barrier alternates, and S of
-        // step i, which the warp has seen, followed the product of step i - 2:
-        // the barrier is in the phase waited for or just past it.
-        auto product_done = [&](uint32_t i) { return warp_wait(&o_full[i & 1], (i >> 1) & 1); };
-        bool ok = true;
-        uint32_t steps = 0, o_ph = 0;
-        int s = next_seg(seg0);
-        if (s < seg1) {
-            load_q(p.w.seg[s]);
-            q_ready();
-        }
-        while (s < seg1 && ok) {
-            const Segment g = p.w.seg[s];
-            const int after = next_seg(s + 1), tiles = g.hi - g.lo;
-            const int tok = token(g);
-            const int len = a.kv_lens[g.n];
-            const int fresh = static_cast<int>(cu_of(a.cu, a.cu64, g.n + 1) - cu_of(a.cu, a.cu64, g.n));
+        // One segment; compiled once for two row tiles and once for one (a common
+        // loop ran 8 % slower on the former).
+        auto segment = [&](uint32_t s, auto two_tiles) {
+            constexpr bool TWO = decltype(two_tiles)::value;
+            const Segment &g = s_seg[s % kSegRing], &ng = s_seg[(s + 1) % kSegRing];
+            const int tiles = g.hi - g.lo;
+            const bool merged = !TWO && tiles > 1;
+            // the row's token in the segment, -1 if it has none
+            const int tile = TWO ? x : 0;
+            const int tok = my_tok < p.tt && tile * p.tt + my_tok < g.ntok ? tile * p.tt + my_tok : -1;
             // keys [from, upto) for this row; rows without a token take what they get
-            const int place = len - fresh + g.j0 + (tok < 0 ? 0 : tok);
-            const int upto = tok < 0 ? 0x7fffffff : a.causal ? place + 1 : len;
+            const int place = g.place + (tok < 0 ? 0 : tok);
+            const int upto = tok < 0 ? 0x7fffffff : a.causal ? place + 1 : g.end;
             const int from = tok >= 0 && a.window >= 0 ? place - a.window : 0;
             const bool idle = !__any_sync(0xffffffffu, tok >= 0);  // no row of the warp has a token
+            constexpr int stride = TWO ? 1 : 2;
+            const int begin = TWO ? 0 : x;
             float m = -INFINITY, l = 0.f;
-            for (int i = 0; i < tiles; ++i, ++steps) {
-                const int buf = NT == 2 ? x : steps & 1;
-                const uint32_t par = NT == 2 ? steps & 1 : (steps >> 1) & 1;
-                ok = warp_wait(&s_full[buf], par);
+            // The next segment's queries, as soon as this segment's last scores
+            // are in: tile 0 by the group that sees them, tile 1 by group 1.
+            bool q0 = false, q1 = false;
+            auto next_q = [&]() {
+                ok = ok && seg_wait(s + 1);
+                if (!ok || ng.tok0 < 0) return;
+                q0 = TWO ? x == 0 : x == ((tiles - 1) & 1);
+                q1 = x == 1 && ng.ntok > p.tt;
+                if (q0) load_q(ng, 0);
+                if (q1) load_q(ng, 1);
+            };
+            if (begin >= tiles) next_q();
+            // the first key of the tile, and the row's keys relative to it
+            int lo = from - (g.lo + begin) * kTile, hi = upto - (g.lo + begin) * kTile;
+            for (int i = begin; i < tiles && ok; i += stride, ++steps, lo -= stride * kTile, hi -= stride * kTile) {
+                ok = warp_wait(&s_full[x], steps & 1);
                 if (!ok) break;
-                if (i == tiles - 1 && after < seg1) load_q(p.w.seg[after]);
+                if (i + stride >= tiles) next_q();
+                // group 1's outputs of the last merged segment have to be read
+                if (x == 1 && i == begin && merges > 0) ok = ok && warp_wait(&o_free, (merges - 1) & 1);
+                if (!ok) break;
                 if (!idle) {
                     tc_fence_after();
                     uint32_t u[4][32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tS(buf) + lanes + 32 * c, u[c]);
+                    for (int c = 0; c < 4; ++c) tmem_ld32(tS(x) + lanes + 32 * c, u[c]);
                     tmem_ld_wait();
-                    const int k0 = (g.lo + i) * kTile;
-                    if (__any_sync(0xffffffffu, k0 < from || upto - k0 < kTile)) {
-                        const int lo = from - k0, hi = upto - k0;
+                    if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
 #pragma unroll
                         for (int c = 0; c < 128; ++c)
                             if (c < lo || c >= hi) u[c >> 5][c & 31] = 0xff800000u;
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 128; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], u[c >> 5][c & 31], u[c >> 5][(c & 31) + 1]);
+                    for (int c = 0; c < 128; c += 2)
+                        mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], u[c >> 5][c & 31], u[c >> 5][(c & 31) + 1]);
                     const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                    if (i == 0) {
+                    if (i == begin) {
                         m = top;
                     } else {
                         // The maximum in use may lag behind the true one by a
@@ -671,11 +802,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             const float f = grow ? ex2((m - top) * sl2) : 1.f;
                             if (grow) m = top;
                             l *= f;
-                            if (NT == 1) {  // the previous product has to be in (NT = 2: S follows it)
-                                ok = product_done(steps - 1);
-                                if (!ok) break;
-                                tc_fence_after();
-                            }
+                            // the stream's last product is in: these scores followed it
 #pragma unroll 1
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t o[32];
@@ -700,11 +827,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             sum2[e & 1] = add2(sum2[e & 1], pair(a0, a1));
                             w[e] = F16 ? pack_f16_rn(a0, a1) : pack_bf2(a0, a1);
                         }
-                        tmem_st16(tS(buf) + lanes + 16 * c, w);
+                        tmem_st16(tS(x) + lanes + 16 * c, w);
                         if (c == 1) {  // the first half of the keys: their product may begin
                             tmem_st_wait();
                             tc_fence_before();
-                            mbar_arrive(&p_half[buf]);
+                            arrive(&p_half[x]);
                         }
                     }
                     const float2 t = unpair(add2(sum2[0], sum2[1]));
@@ -712,50 +839,98 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                 } else {
-                    mbar_arrive(&p_half[buf]);
+                    arrive(&p_half[x]);
                 }
-                mbar_arrive(&p_full[buf]);
+                arrive(&p_full[x]);
             }
-            if (!ok) break;
-            if (after < seg1) q_ready();
-            ok = NT == 2 ? warp_wait(&o_full[x], o_ph) : product_done(steps - 1);
-            if (!ok) break;
-            o_ph ^= 1;
-            tc_fence_after();
-            if (!idle) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                bf16 *o = tok >= 0 && g.slot < 0 ? out_row(g, tok) : nullptr;
-                float *po = p.w.part_o + (static_cast<int64_t>(g.slot) * NT * kTile + x * kTile + row) * D;
+            if (!ok) return;
+            q_ready(q0, q1);
+            if (merged && x == 1) {  // group 0 merges
+                s_ml[row] = make_float2(m, l);
+                arrive(&ml_full);
+            }
+            if (TWO || x == 0) {
+                ok = warp_wait(&o_full[x], o_ph[x] & 1);
+                float f0 = 1.f, f1 = 0.f;
+                if (merged) {
+                    ok = ok && warp_wait(&o_full[1], o_ph[1] & 1) && warp_wait(&ml_full, merges & 1);
+                    const float2 ml = s_ml[row];
+                    const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top * sl2;
+                    f0 = ex2(fmaf(m, sl2, -base));
+                    f1 = ex2(fmaf(ml.x, sl2, -base));
+                    m = top;
+                    l = f0 * l + f1 * ml.y;
+                }
+                if (!ok) return;
+                tc_fence_after();
+                if (!idle) {
+                    const bool whole = g.slot < 0;
+                    const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                    const int head = g.h * a.G + my_head;
+                    const int64_t tok_row = static_cast<int64_t>(g.tok0) + max(tok, 0);
+                    bf16 *o = a.out + tok_row * a.so_t + head * a.so_h;
+                    const int64_t part = static_cast<int64_t>(max(g.slot, 0)) * 2 * kTile + tile * kTile + row;
+                    float *po = p.part_o + part * D;
+                    f0 *= inv;
+                    f1 *= inv;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t u[32];
-                    tmem_ld32(tO(x) + lanes + c, u);
-                    tmem_ld_wait();
-                    if (tok >= 0 && g.slot < 0) {
+                    for (int c = 0; c < D; c += 32) {
+                        __syncwarp();
+                        uint32_t u[32];
+                        tmem_ld32(tO(x) + lanes + c, u);
+                        tmem_ld_wait();
+                        if (merged) {
+                            uint32_t v[32];
+                            tmem_ld32(tO(1) + lanes + c, v);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
+                            for (int e = 0; e < 32; ++e)
+                                u[e] = __float_as_uint(__uint_as_float(u[e]) * f0 + __uint_as_float(v[e]) * f1);
+                        } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float y = __uint_as_float(u[e + 2 * k]) * inv, z = __uint_as_float(u[e + 2 * k + 1]) * inv;
-                                w[k] = F16 ? pack_f16_rn(y, z) : pack_bf2(y, z);
-                            }
-                            *reinterpret_cast<uint4 *>(o + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f0);
                         }
-                    } else if (tok >= 0) {
+                        if (tok < 0) continue;
+                        if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(po + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                            for (int e = 0; e < 32; e += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float y = __uint_as_float(u[e + 2 * k]), z = __uint_as_float(u[e + 2 * k + 1]);
+                                    w[k] = F16 ? pack_f16_rn(y, z) : pack_bf2(y, z);
+                                }
+                                *reinterpret_cast<uint4 *>(o + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(po + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                        }
                     }
+                    const float base = m == -INFINITY ? -INFINITY : m * sl2;
+                    if (tok >= 0 && !whole)
+                        p.part_ml[part] = make_float2(base, l);
+                    else if (tok >= 0 && a.lse)
+                        a.lse[tok_row * a.HQ + head] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
                 }
-                const float base = m == -INFINITY ? -INFINITY : m * sl2;
-                if (tok >= 0 && g.slot < 0)
-                    put_lse(g, tok, l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2);
-                else if (tok >= 0)
-                    p.w.part_ml[static_cast<int64_t>(g.slot) * NT * kTile + x * kTile + row] = make_float2(base, l);
+                tc_fence_before();
+                if (merged) arrive(&o_free);
             }
-            tc_fence_before();
-            s = after;
+            o_ph[0] += 1;
+            o_ph[1] += TWO || merged;
+            merges += merged;
+        };
+        for (uint32_t s = 0; ok; ++s) {
+            const Segment &g = s_seg[s % kSegRing];
+            if (g.tok0 < 0) break;
+            if (g.ntok > p.tt)
+                segment(s, std::true_type());
+            else
+                segment(s, std::false_type());
+            seg_done(s);
+            // the next segment's description, for a group that had no tiles here
+            ok = ok && seg_wait(s + 1);
         }
         if (!ok) fail();
         cp_async_wait_all();
@@ -763,34 +938,45 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         few_regs();
     }
     __syncthreads();
-    if (wp == C::kMmaWarp) {
+    if (wp == kMmaWarp) {
         tmem_relinquish();
         tmem_dealloc(tm, 512);
     }
+    if (tid == 0) p.flags[blockIdx.x] = s_share.flags;
 }
 
 // ---------------------------------------------------------------- combine
 // Rows of the items that were cut: a warp per row,
 //   M = max_i m_i,  L = sum_i 2^(m_i - M) l_i,  o = sum_i 2^(m_i - M) o_i / L.
-constexpr int kJoinRows = 16;  // rows of a block: 4 warps, 4 rows each
+// The first block also gathers the CTAs' flags into the status words.
+constexpr int kJoinRows = 32;  // rows of a block: 8 warps, 4 rows each
 
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(128) gdn2_attn_combine_kernel(const __grid_constant__ KernelParams p) {
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) gdn2_attn_combine_kernel(const __grid_constant__ KernelParams p) {
     constexpr int E = D / 32;  // channels of a lane
     const AttnParams &a = p.a;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     pdl_wait();
-    const Joint j = p.w.joint[blockIdx.x];
+    if (blockIdx.x == 0 && blockIdx.y == 0 && wp == 0) {
+        int f = 0;
+        for (int c = lane; c < static_cast<int>(gridDim.x); c += 32) f |= p.flags[c];
+        f = __reduce_or_sync(0xffffffffu, f);
+        if (lane < 8)
+            a.status[lane] = lane == 0   ? f & kBadCu ? GDN2_ERR_CU_SEQLENS : f & kBadPages ? GDN2_ERR_PAGES : GDN2_OK
+                             : lane == 2 ? f & kTimeout ? GDN2_ERR_TIMEOUT : GDN2_OK
+                                         : 0;
+    }
+    const Joint j = p.joint[blockIdx.x];
     if (j.more <= 0) return;
-    const int64_t t0 = cu_of(a.cu, a.cu64, j.n) + j.j0;
-    for (int i = wp; i < kJoinRows; i += 4) {
+    for (int i = wp; i < kJoinRows; i += 8) {
         const int r = blockIdx.y * kJoinRows + i, x = r / kTile, rr = r % kTile;
         const int tk = rr / a.G, tok = x * p.tt + tk, hd = rr - tk * a.G;
         if (tk >= p.tt || tok >= j.ntok) continue;
-        auto slot = [&](int k) { return k == 0 ? j.slot : 2 * (static_cast<int>(blockIdx.x) + k); };
-        auto at = [&](int k) { return static_cast<int64_t>(slot(k)) * NT * kTile + r; };
+        auto at = [&](int k) {
+            return static_cast<int64_t>(k == 0 ? j.slot : 2 * (static_cast<int>(blockIdx.x) + k)) * 2 * kTile + r;
+        };
         float M = -INFINITY;
-        for (int k = lane; k <= j.more; k += 32) M = fmaxf(M, p.w.part_ml[at(k)].x);
+        for (int k = lane; k <= j.more; k += 32) M = fmaxf(M, p.part_ml[at(k)].x);
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         const float base = M == -INFINITY ? 0.f : M;
         float L = 0.f, acc[E];
@@ -799,7 +985,7 @@ __global__ void __launch_bounds__(128) gdn2_attn_combine_kernel(const __grid_con
         for (int k0 = 0; k0 <= j.more; k0 += 32) {
             float w = 0.f, l = 0.f;
             if (k0 + lane <= j.more) {
-                const float2 ml = p.w.part_ml[at(k0 + lane)];
+                const float2 ml = p.part_ml[at(k0 + lane)];
                 w = ex2(ml.x - base);
                 l = w * ml.y;
             }
@@ -809,7 +995,7 @@ __global__ void __launch_bounds__(128) gdn2_attn_combine_kernel(const __grid_con
 #pragma unroll 4
             for (int k = 0; k < cnt; ++k) {
                 const float wk = __shfl_sync(0xffffffffu, w, k);
-                const float *o = p.w.part_o + at(k0 + k) * D + lane * E;
+                const float *o = p.part_o + at(k0 + k) * D + lane * E;
                 if (E == 4) {
                     const float4 v = *reinterpret_cast<const float4 *>(o);
                     acc[0] += wk * v.x; acc[1] += wk * v.y; acc[E - 2] += wk * v.z; acc[E - 1] += wk * v.w;
@@ -820,8 +1006,9 @@ __global__ void __launch_bounds__(128) gdn2_attn_combine_kernel(const __grid_con
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int h = j.h * a.G + hd;
-        bf16 *o = a.out + (t0 + tok) * a.so_t + h * a.so_h + lane * E;
+        const int head = j.h * a.G + hd;
+        const int64_t tok_row = static_cast<int64_t>(j.tok0) + tok;
+        bf16 *o = a.out + tok_row * a.so_t + head * a.so_h + lane * E;
         uint32_t w[E / 2];
 #pragma unroll
         for (int e = 0; e < E / 2; ++e)
@@ -830,7 +1017,7 @@ __global__ void __launch_bounds__(128) gdn2_attn_combine_kernel(const __grid_con
             *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[E / 2 - 1]);
         else
             *reinterpret_cast<uint32_t *>(o) = w[0];
-        if (a.lse && lane == 0) a.lse[(t0 + tok) * a.HQ + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        if (a.lse && lane == 0) a.lse[tok_row * a.HQ + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
 }
 
@@ -881,15 +1068,15 @@ bool encode_cache(CUtensorMap *map, int (&pos)[3], const void *base, const AttnP
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT, bool F16>
+template <int D, bool F16>
 cudaError_t launch(const KernelParams &p, int ctas, cudaStream_t s) {
-    using C = Cfg<D, NT>;
-    auto kern = gdn2_paged_attn_kernel<D, NT, F16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    auto kern = gdn2_paged_attn_kernel<D, F16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_chained(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, s, p);
+    kern<<<ctas, kThreads, Cfg<D>::kSmem, s>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_chained(gdn2_attn_combine_kernel<D, NT, F16>, dim3(ctas, NT * kTile / kJoinRows), dim3(128), 0, s, p);
+    return launch_chained(gdn2_attn_combine_kernel<D, F16>, dim3(ctas, 2 * kTile / kJoinRows), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -898,18 +1085,15 @@ size_t paged_attn_workspace(const gdn2_attn_dims &d) { return layout_of(d).total
 
 cudaError_t launch_paged_attn(const AttnParams &a, const gdn2_attn_dims &d, int sms, void *workspace, cudaStream_t s) {
     const bool f16 = d.dtype == GDN2_DTYPE_F16;
-    const int nt = row_tiles(d), ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
     const Layout l = layout_of(d);
     char *ws = static_cast<char *>(workspace);
     KernelParams p;
     p.a = a;
-    p.w.first = reinterpret_cast<int *>(ws + l.first);
-    p.w.last = reinterpret_cast<int *>(ws + l.last);
-    p.w.joint = reinterpret_cast<Joint *>(ws + l.joint);
-    p.w.seq = reinterpret_cast<SeqPlan *>(ws + l.seq);
-    p.w.seg = reinterpret_cast<Segment *>(ws + l.seg);
-    p.w.part_o = reinterpret_cast<float *>(ws + l.part_o);
-    p.w.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
+    p.flags = reinterpret_cast<int *>(ws + l.flags);
+    p.joint = reinterpret_cast<Joint *>(ws + l.joint);
+    p.part_o = reinterpret_cast<float *>(ws + l.part_o);
+    p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.scale_log2 = a.scale * kLog2e;
     p.tt = kTile / a.G;
     p.granule = 8;
@@ -917,15 +1101,8 @@ cudaError_t launch_paged_attn(const AttnParams &a, const gdn2_attn_dims &d, int 
     if (a.T > 0 && (!encode_cache(&p.tk, p.kpos, a.k_cache, a, a.skc, d.D, f16, p.granule) ||
                     !encode_cache(&p.tv, p.vpos, a.v_cache, a, a.svc, d.D, f16, p.granule)))
         return cudaErrorInvalidValue;
-    gdn2_attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, ctas, nt);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.T == 0) return e;
-    if (d.D == 64) {
-        if (nt == 1) return f16 ? launch<64, 1, true>(p, ctas, s) : launch<64, 1, false>(p, ctas, s);
-        return f16 ? launch<64, 2, true>(p, ctas, s) : launch<64, 2, false>(p, ctas, s);
-    }
-    if (nt == 1) return f16 ? launch<128, 1, true>(p, ctas, s) : launch<128, 1, false>(p, ctas, s);
-    return f16 ? launch<128, 2, true>(p, ctas, s) : launch<128, 2, false>(p, ctas, s);
+    if (d.D == 64) return f16 ? launch<64, true>(p, ctas, s) : launch<64, false>(p, ctas, s);
+    return f16 ? launch<128, true>(p, ctas, s) : launch<128, false>(p, ctas, s);
 }
 
 }  // namespace gdn2
