@@ -21,8 +21,13 @@
 //   warp 8          issues the products (tcgen05): S = Q K^T into Tensor Memory
 //                   (fp32), O += P V with P from Tensor Memory (16 bits)
 //   warp 9          walks the share, hands the segments out through a ring in
-//                   shared memory, and loads keys and values by TMA, straight
-//                   from their pages, into a ring of 128-key stages
+//                   shared memory, and loads the keys by TMA, straight from their
+//                   pages, into a ring of 128-key stages
+//   warp 10         loads the values into the same ring (lanes that issue TMA
+//                   copies take turns, 50 cycles each: with small pages one warp
+//                   for both bound decode to 79 % of the bandwidth)
+//   warp 11         loads the queries as soon as the last scores of the segment
+//                   before are in
 // With two row tiles in an item, group x has tile x and both read every stage;
 // with one (decode), group x has every second key tile, with statistics and
 // outputs of its own that are merged at the end of the segment.  Either way one
@@ -45,7 +50,7 @@ using namespace tc;
 constexpr int kMaxCtas = 152;   // shares at most (SMs of a GB300)
 constexpr int kTile = 128;      // rows of a tile, keys of a tile
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
 constexpr int kSegRing = 8;     // segments in flight between the warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -61,6 +66,7 @@ struct __align__(16) Segment {
     int lo, hi;
     int end;    // keys from `end` on are not attended to
     int place;  // of the first new token in its cached sequence
+    int seq, pad[3];
 };
 // The item whose pieces the combine kernel joins: the first in slot `slot`,
 // then `more` in slots 2 (cta + 1), 2 (cta + 2), ...
@@ -80,7 +86,8 @@ struct KernelParams {
     int tt;                      // tokens per row tile: 128 / G
     int granule;                 // keys per TMA box
     int kpos[3], vpos[3];        // coordinate (1 .. 3) of page, token, head in the tensor maps
-    CUtensorMap tk, tv;
+    int q_map;                   // tq is set: the queries come by TMA
+    CUtensorMap tk, tv, tq;
 };
 
 struct Layout {
@@ -118,6 +125,41 @@ __device__ __forceinline__ int item_cost(const AttnParams &a, int len, int fresh
     return max(1, s.hi - s.lo);
 }
 
+// sum over i < n of floor((a i + b) / 128), a, b >= 0.
+__device__ long long floor_sum(long long n, long long a, long long b) {
+    long long m = 128, sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            sum += (n - 1) * n / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const long long top = a * n + b;
+        if (top < m) break;
+        n = top / m;
+        b = top % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+// Whether the costs of a sequence's items add up in closed form.
+__device__ __forceinline__ bool closed_form(const AttnParams &a, int len, int fresh) {
+    return !a.causal || (a.window < 0 && len >= fresh);
+}
+// The cost of a sequence's first `items` items.
+__device__ long long cost_of(const AttnParams &a, int len, int fresh, int tokens, int items) {
+    if (items <= 0) return 0;
+    if (!a.causal) return static_cast<long long>(items) * max(1, (len + kTile - 1) / kTile);
+    // item m: ceil((len - fresh + min(fresh, (m + 1) tokens)) / 128); the last one apart
+    const long long last = (len - fresh + min(static_cast<long long>(fresh), static_cast<long long>(items) * tokens) + kTile - 1) / kTile;
+    return last + floor_sum(items - 1, tokens, static_cast<long long>(len) - fresh + tokens + kTile - 1);
+}
+
 __device__ __forceinline__ long long div_by(long long x, long long y) {
     return (x | y) >> 32 ? x / y : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
 }
@@ -147,7 +189,9 @@ __device__ __forceinline__ Seq seq_at(const AttnParams &a, int n, int *flags) {
 __device__ long long seq_cost(const AttnParams &a, int n, int tokens, int *flags) {
     const int lane = threadIdx.x & 31;
     const Seq q = seq_at(a, n, flags);
-    long long cost = q.fresh == 0 ? 0 : q.fresh <= tokens ? item_cost(a, q.len, q.fresh, tokens, 0) : -1;
+    long long cost = q.fresh == 0 ? 0 : q.fresh <= tokens ? item_cost(a, q.len, q.fresh, tokens, 0)
+                     : closed_form(a, q.len, q.fresh) ? cost_of(a, q.len, q.fresh, tokens, (q.fresh + tokens - 1) / tokens)
+                                                      : -1;
     for (uint32_t more = __ballot_sync(0xffffffffu, cost < 0); more; more &= more - 1) {
         const int src = __ffs(more) - 1;
         const int len = __shfl_sync(0xffffffffu, q.len, src), fresh = __shfl_sync(0xffffffffu, q.fresh, src);
@@ -164,11 +208,12 @@ struct Share {
     long long total, shares;
     long long in_seq, cost;  // offset of the first tile in its sequence, the sequence's cost per head
     int n, flags;            // sequence of the first tile
+    long long part[kThreads / 32];
 };
 
 // The share of this CTA; every thread of the block calls it, s is in shared memory.
 __device__ void find_share(const AttnParams &a, int tokens, Share &s) {
-    __shared__ long long part[kThreads / 32];
+    long long *const part = s.part;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
     int flags = 0;
     if (tid == 0) {
@@ -249,6 +294,19 @@ struct Walk {
         long long at = s.in_seq - h * s.cost;
         // the item that holds tile `at` of the head
         const int lane = threadIdx.x & 31;
+        if (items > 32 && closed_form(a, q.len, q.fresh)) {
+            // narrow down to 32 items: lanes try as many places at once
+            int lo = 0, hi = items;
+            while (hi - lo > 32) {
+                const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+                const uint32_t before = __ballot_sync(0xffffffffu, i < hi && cost_of(a, q.len, q.fresh, tokens, i) <= at);
+                const int k = 31 - __clz(before | 1);
+                lo += k * step;
+                hi = min(hi, lo + step);
+            }
+            at -= cost_of(a, q.len, q.fresh, tokens, lo);
+            m = lo;
+        }
         for (;; m += 32) {
             const int cost = m + lane < items ? item_cost(a, q.len, q.fresh, tokens, m + lane) : 0;
             int sum = cost;
@@ -269,14 +327,14 @@ struct Walk {
     }
     // The next segment; false at the end.  `cut`: it ends before its item does,
     // by `rest` key tiles.
-    __device__ bool next(Segment &g, int &rest, int &seq) {
+    __device__ bool next(Segment &g, int &rest) {
         rest = 0;
         if (left <= 0) return false;
         const int j0 = m * tokens;
         const Span s = key_span(a, q.len, q.fresh, j0, min(q.fresh, j0 + tokens));
         const int cost = max(1, s.hi - s.lo);
         const int take = static_cast<int>(min(static_cast<long long>(cost - off), left));
-        seq = n;
+        g.seq = n;
         g.tok0 = q.t0 + j0;
         g.h = h;
         g.ntok = min(tokens, q.fresh - j0);
@@ -307,13 +365,29 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------- main
+// What the warps share besides the tiles.
+template <int STAGES>
+struct Small {
+    uint64_t full[STAGES], empty[STAGES], tail, drain;
+    uint64_t seg_full[kSegRing], seg_empty[kSegRing];
+    uint64_t q_full[2], q_free[2];                     // of row tile t
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2];  // of stream x
+    uint64_t ml_full, o_free;  // one row tile: group 1's statistics are in; group 0 has read the outputs
+    Segment seg[kSegRing];
+    Share share;
+    float2 ml[kTile];
+    uint32_t tmem;
+};
+
 template <int D>
 struct Cfg {
     static constexpr int kStageBytes = kTile * D * 2;
     static constexpr int kQBytes = kTile * D * 2;
     static constexpr int kStages = D == 128 ? 5 : 10;  // what fits beside the query tiles
     static constexpr int kRing = 2 * kQBytes;
-    static constexpr int kSmem = kRing + kStages * kStageBytes + 1024;  // + alignment slack
+    static constexpr int kShared = kRing + kStages * kStageBytes;  // the barriers and small arrays
+    static constexpr int kSmem = kShared + static_cast<int>(sizeof(Small<kStages>));
+    static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, const int (&c)[4], uint64_t *bar) {
@@ -322,6 +396,35 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, c
         "%5}], [%6];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]), "r"(smem_u32(bar))
         : "memory");
+}
+
+// Tensor Memory in the shape of 16 lanes, 64 columns: thread t has lanes t / 4 (h =
+// 0) and t / 4 + 8 (h = 1) of the 16 from the address's lane on, r[4 n + 2 h + e] =
+// column 8 n + 2 (t % 4) + e.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+// Thread q of a quad gives w[k] to thread k and gets thread k's w[q] as w[k].
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
+    const bool odd = q & 1, high = q & 2;
+    uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), b = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+    // pairs of group q & 1 and of group 2 + (q & 1)
+    uint32_t lo0 = odd ? a : w[0], lo1 = odd ? w[1] : a, hi0 = odd ? b : w[2], hi1 = odd ? w[3] : b;
+    a = __shfl_xor_sync(0xffffffffu, high ? lo0 : hi0, 2);
+    b = __shfl_xor_sync(0xffffffffu, high ? lo1 : hi1, 2);
+    w[0] = high ? a : lo0;
+    w[1] = high ? b : lo1;
+    w[2] = high ? hi0 : a;
+    w[3] = high ? hi1 : b;
 }
 
 // One thread of the warp, the same each time.
@@ -368,14 +471,20 @@ __device__ __forceinline__ float2 unpair(uint64_t x) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
     return r;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// The same, and 2^x, kept in the order in which they are written.
+__device__ __forceinline__ uint64_t fma2_here(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float ex2_here(float x) {
+    float r;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
@@ -384,23 +493,29 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
     return r;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __grid_constant__ KernelParams p) {
     using C = Cfg<D>;
     constexpr int NB = D / 64;  // 64-channel blocks of a row
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], tail, drain;
-    __shared__ uint64_t seg_full[kSegRing], seg_empty[kSegRing];
-    // of row tile (q_full) or stream (the others) x
-    __shared__ uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
-    __shared__ uint64_t ml_full, o_free;  // one row tile: group 1's statistics are in; group 0 has read the outputs
-    __shared__ Segment s_seg[kSegRing];
-    __shared__ float2 s_ml[kTile];
-    __shared__ Share s_share;
-    __shared__ uint32_t s_tmem;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Small<C::kStages> &sh = *reinterpret_cast<Small<C::kStages> *>(smem + C::kShared);
+    uint64_t *const full = sh.full, *const empty = sh.empty;
     const AttnParams &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+    // The 128-byte swizzle goes by address: the dynamic shared memory, the only
+    // one of this kernel, has to begin on a 1024-byte boundary, as it does (the
+    // room left does not allow for slack).  Checked all the same.
+    if (smem_u32(smem) & 1023) {
+        if (tid == 0) {
+            p.flags[blockIdx.x] = kTimeout;
+            p.joint[blockIdx.x].more = 0;
+        }
+        return;
+    }
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -408,69 +523,155 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kSegRing; ++i) {
-            mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 9);  // 8 softmax warps and the issuing one
+            mbar_init(&sh.seg_full[i], 1);
+            mbar_init(&sh.seg_empty[i], 11);  // the warps but the one that hands them out
         }
-        mbar_init(&tail, 1);
-        mbar_init(&drain, 1);
+        mbar_init(&sh.tail, 1);
+        mbar_init(&sh.drain, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 4);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_half[i], 4);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_free[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_half[i], 4);
+            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.o_full[i], 1);
         }
-        mbar_init(&ml_full, 4);
-        mbar_init(&o_free, 4);
+        mbar_init(&sh.ml_full, 4);
+        mbar_init(&sh.o_free, 4);
         fence_mbar_init();
     }
-    if (wp == kMmaWarp) tmem_alloc(&s_tmem, 512);
+    if (wp == kMmaWarp) tmem_alloc(&sh.tmem, 512);
+    if (tid == 32 * kKeyWarp && a.T > 0) {
+        prefetch_map(&p.tk);
+        prefetch_map(&p.tv);
+        if (p.q_map) prefetch_map(&p.tq);
+    }
     pdl_trigger();
-    find_share(a, 2 * p.tt, s_share);
+    find_share(a, 2 * p.tt, sh.share);
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = s_tmem;
+    const uint32_t tm = sh.tmem;
     const uint32_t sQ = smem_u32(smem), sRing = smem_u32(smem + C::kRing);
     // Tensor Memory columns: scores of stream x at 128 x, its outputs after them
     auto tS = [&](int x) { return tm + 128 * x; };
     auto tO = [&](int x) { return tm + 256 + 128 * x; };
-    auto fail = [&]() { atomicOr(&s_share.flags, kTimeout); };
+    auto fail = [&]() { atomicOr(&sh.share.flags, kTimeout); };
     auto few_regs = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); };
     // the i-th segment of the share; its last reader in a warp releases it
-    auto seg_wait = [&](uint32_t i) { return warp_wait(&seg_full[i % kSegRing], (i / kSegRing) & 1); };
+    auto seg_wait = [&](uint32_t i) { return warp_wait(&sh.seg_full[i % kSegRing], (i / kSegRing) & 1); };
     auto seg_done = [&](uint32_t i) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[i % kSegRing]);
+        if (lane == 0) mbar_arrive(&sh.seg_empty[i % kSegRing]);
     };
 
-    if (wp == kTmaWarp) {
-        // ----------------------------- segments; keys and values by TMA
-        few_regs();
+    // Keys or values of a segment's tiles into the ring, by one warp.  `at`: the
+    // place of tile i's load among the segment's 2 x tiles, in the order in which
+    // the products take them: K0 V0 K1 V1 .. with two row tiles, with one the keys
+    // run two tiles ahead of the values.  The releases come in the same order, so
+    // that a stage's emptiness is never mistaken for an earlier one's.
+    auto key_at = [](int i, bool two) { return two ? 2 * i : i < 2 ? i : 2 * i - 1; };
+    auto value_at = [](int i, int tiles, bool two) { return two ? 2 * i + 1 : i <= tiles - 2 ? 2 + 2 * i : 2 * tiles - 1; };
+    struct Loader {
+        uint32_t base = 0, used = 0;  // loads of the segments before; one past this warp's last
+        int tail_ph = 0;
+        bool ok = true;
+    };
+    auto load_tiles = [&](Loader &ld, const Segment &g, bool is_v, auto at, auto ahead) {
         const int gran = p.granule, per = kTile / gran;     // granules of a tile
         const int batch = 32 / per;                         // tiles whose table entries one load fetches
         const int my_gr = lane / NB, my_cb = lane % NB;     // this lane's granule and channel block
-        uint32_t loads = 0;                                 // tiles loaded so far
-        uint32_t pushed = 0;                                // segments handed out
-        int tail_ph = 0;
-        bool ok = true;
+        const int tiles = g.hi - g.lo;
+        const int *row = a.table + static_cast<int64_t>(g.seq) * a.table_stride;
+        const int *pos = is_v ? p.vpos : p.kpos;
+        // page and slot of this lane's granule of the batch that starts at tile t
+        auto fetch = [&](int t) {
+            t += lane / per;
+            int2 e = make_int2(0, 0);
+            const int64_t key = static_cast<int64_t>(t) * kTile + (lane % per) * gran;
+            if (t < g.hi && key < g.end) {
+                const int col = static_cast<int>(key) / a.page_size;
+                e = make_int2(row[col], static_cast<int>(key) - col * a.page_size);
+                if (e.x < 0 || e.x >= a.num_pages) {
+                    e.x = static_cast<int>(a.num_pages);  // past the tensor: the box reads zeros
+                    atomicOr(&sh.share.flags, kBadPages);
+                }
+            }
+            return e;
+        };
+        int2 now = fetch(g.lo), next = fetch(g.lo + batch);
+        ahead();
+        for (int i = 0, in = 0; i < tiles && ld.ok; ++i) {
+            const uint32_t load = ld.base + at(i);
+            const int st = static_cast<int>(load % C::kStages);
+            const int left = min(kTile, g.end - (g.lo + i) * kTile);  // rows that count
+            const int grans = (left + gran - 1) / gran;
+            ld.ok = warp_wait(&empty[st], ((load / C::kStages) & 1) ^ 1);
+            if (!ld.ok) return;
+            const bool patch = is_v && left < kTile;
+            uint64_t *bar = patch ? &sh.tail : &full[st];
+            uint8_t *dst = smem + C::kRing + st * C::kStageBytes;
+            if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(grans * gran * 128 * NB));
+            __syncwarp();
+            const int from = in * per + min(my_gr, per - 1);
+            const int page = __shfl_sync(0xffffffffu, now.x, from), slot = __shfl_sync(0xffffffffu, now.y, from);
+            if (my_gr < grans) {
+                int c[4] = {my_cb * 64, 0, 0, 0};
+#pragma unroll
+                for (int k = 1; k < 4; ++k) c[k] = pos[0] == k ? page : pos[1] == k ? slot : g.h;
+                tma_load_4d(dst + my_cb * (kTile * 128) + my_gr * gran * 128, is_v ? &p.tv : &p.tk, c, bar);
+            }
+            ld.used = load + 1;
+            if (patch) {  // zero the rows past the range, once the copies are in
+                ld.ok = warp_wait(&sh.tail, ld.tail_ph);
+                if (!ld.ok) return;
+                ld.tail_ph ^= 1;
+                for (int k = lane; k < (kTile - left) * NB * 8; k += 32) {
+                    const int r = left + k / (NB * 8), q = k % (NB * 8);
+                    *reinterpret_cast<uint4 *>(dst + (q >> 3) * (kTile * 128) + r * 128 + (q & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[st]);
+            }
+            if (++in == batch) {
+                in = 0;
+                now = next;
+                next = fetch(g.lo + i + 1 + batch);
+            }
+        }
+        ld.base += 2 * tiles;
+    };
+    // a loader that gave up lets its copies in flight land before the block ends
+    auto settle = [&](const Loader &ld) {
+        if (ld.ok) return;
+        if (lane == 0) fail();
+        for (uint32_t i = ld.used > C::kStages ? ld.used - C::kStages : 0; i < ld.used; ++i)
+            warp_wait(&full[i % C::kStages], (i / C::kStages) & 1);
+    };
+
+    if (wp == kKeyWarp) {
+        // ----------------------------------------------- segments and keys
+        few_regs();
+        uint32_t pushed = 0;  // segments handed out
         Joint joint = {};
-        Walk walk(a, 2 * p.tt, s_share);
+        Loader ld;
+        Walk walk(a, 2 * p.tt, sh.share);
         // The next segment that has keys, handed out; the others' rows are
         // written here.  tok0 = -1 ends the share.
         Segment g;
-        int seq;
         auto hand_out = [&]() {
             for (;;) {
                 int rest;
-                if (!walk.next(g, rest, seq)) {
+                if (!walk.next(g, rest)) {
                     g.tok0 = -1;
                     break;
                 }
                 if (rest > 0) {
                     // the item goes on in the shares that its last tile reaches
                     joint = {g.tok0, g.h, g.ntok, g.slot, 0, {0, 0, 0}};
-                    const long long last = s_share.begin + s_share.left + rest - 1;
-                    joint.more = static_cast<int>(div_by((last + 1) * s_share.shares - 1, s_share.total)) - static_cast<int>(blockIdx.x);
+                    const long long last = sh.share.begin + sh.share.left + rest - 1;
+                    joint.more = static_cast<int>(div_by((last + 1) * sh.share.shares - 1, sh.share.total)) - static_cast<int>(blockIdx.x);
                 }
                 if (g.hi > g.lo) break;
                 for (int i = lane; i < g.ntok * a.G; i += 32) {
@@ -481,217 +682,199 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     if (a.lse) a.lse[tok * a.HQ + head] = -INFINITY;
                 }
             }
-            ok = warp_wait(&seg_empty[pushed % kSegRing], ((pushed / kSegRing) & 1) ^ 1);
-            if (!ok) return;
+            ld.ok = ld.ok && warp_wait(&sh.seg_empty[pushed % kSegRing], ((pushed / kSegRing) & 1) ^ 1);
+            if (!ld.ok) return;
             if (lane == 0) {
-                s_seg[pushed % kSegRing] = g;
-                mbar_arrive(&seg_full[pushed % kSegRing]);
+                sh.seg[pushed % kSegRing] = g;
+                mbar_arrive(&sh.seg_full[pushed % kSegRing]);
             }
             __syncwarp();
             ++pushed;
         };
         hand_out();
-        while (ok && g.tok0 >= 0) {
+        while (ld.ok && g.tok0 >= 0) {
             const Segment cur = g;
-            const int tiles = cur.hi - cur.lo;
-            const int *row = a.table + static_cast<int64_t>(seq) * a.table_stride;
-            // page and slot of this lane's granule of the batch that starts at tile t
-            auto fetch = [&](int t) {
-                t += lane / per;
-                int2 e = make_int2(0, 0);
-                const int64_t key = static_cast<int64_t>(t) * kTile + (lane % per) * gran;
-                if (t < cur.hi && key < cur.end) {
-                    const int col = static_cast<int>(key) / a.page_size;
-                    e = make_int2(row[col], static_cast<int>(key) - col * a.page_size);
-                    if (e.x < 0 || e.x >= a.num_pages) {
-                        e.x = static_cast<int>(a.num_pages);  // past the tensor: the box reads zeros
-                        atomicOr(&s_share.flags, kBadPages);
-                    }
-                }
-                return e;
-            };
-            // entries of the batch that the values are in, and of the next
-            int at = 0;
-            int2 now = fetch(cur.lo), next = fetch(cur.lo + batch);
-            hand_out();  // one segment ahead, so that its queries can be loaded early
-            // keys or values of tile lo + i into the next stage
-            auto load = [&](int i, bool is_v) {
-                const int st = static_cast<int>(loads % C::kStages);
-                const int left = min(kTile, cur.end - (cur.lo + i) * kTile);  // rows that count
-                const int grans = (left + gran - 1) / gran;
-                ok = ok && warp_wait(&empty[st], ((loads / C::kStages) & 1) ^ 1);
-                if (!ok) return;
-                const bool patch = is_v && left < kTile;
-                uint64_t *bar = patch ? &tail : &full[st];
-                uint8_t *dst = smem + C::kRing + st * C::kStageBytes;
-                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(grans * gran * 128 * NB));
-                __syncwarp();
-                const int2 e = i / batch == at ? now : next;
-                const int from = i % batch * per + min(my_gr, per - 1);
-                const int page = __shfl_sync(0xffffffffu, e.x, from), slot = __shfl_sync(0xffffffffu, e.y, from);
-                if (my_gr < grans) {
-                    const int *pos = is_v ? p.vpos : p.kpos;
-                    int c[4] = {my_cb * 64, 0, 0, 0};
-#pragma unroll
-                    for (int k = 1; k < 4; ++k) c[k] = pos[0] == k ? page : pos[1] == k ? slot : cur.h;
-                    tma_load_4d(dst + my_cb * (kTile * 128) + my_gr * gran * 128, is_v ? &p.tv : &p.tk, c, bar);
-                }
-                ++loads;
-                if (patch) {  // zero the rows past the range, once the copies are in
-                    ok = warp_wait(&tail, tail_ph);
-                    if (!ok) return;
-                    tail_ph ^= 1;
-                    for (int k = lane; k < (kTile - left) * NB * 8; k += 32) {
-                        const int r = left + k / (NB * 8), q = k % (NB * 8);
-                        *reinterpret_cast<uint4 *>(dst + (q >> 3) * (kTile * 128) + r * 128 + (q & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[st]);
-                }
-                if (is_v && (i + 1) % batch == 0) {
-                    now = next;
-                    next = fetch(cur.lo + (++at + 1) * batch);
-                }
-            };
-            // in the order in which the products take them: with one row tile
-            // the keys run two tiles ahead of the values
-            if (cur.ntok > p.tt) {
-                for (int i = 0; i < tiles && ok; ++i) {
-                    load(i, false);
-                    load(i, true);
-                }
-            } else {
-                load(0, false);
-                if (tiles > 1) load(1, false);
-                for (int i = 0; i < tiles && ok; ++i) {
-                    load(i, true);
-                    if (i + 2 < tiles) load(i + 2, false);
-                }
-            }
+            const bool two = cur.ntok > p.tt;
+            // (the next one is handed out before this one's copies, so that its
+            // queries can be loaded early)
+            load_tiles(ld, cur, false, [&](int i) { return key_at(i, two); }, hand_out);
         }
         if (lane == 0) p.joint[blockIdx.x] = joint;
-        if (!ok) {
-            if (lane == 0) fail();
-            // let the copies in flight land before the block ends
-            for (uint32_t i = loads > C::kStages ? loads - C::kStages : 0; i < loads; ++i)
-                warp_wait(&full[i % C::kStages], (i / C::kStages) & 1);
+        settle(ld);
+    } else if (wp == kValueWarp) {
+        // ---------------------------------------------------------- values
+        few_regs();
+        Loader ld;
+        for (uint32_t s = 0; ld.ok; ++s) {
+            ld.ok = seg_wait(s);
+            if (!ld.ok || sh.seg[s % kSegRing].tok0 < 0) break;
+            const Segment cur = sh.seg[s % kSegRing];
+            seg_done(s);
+            const bool two = cur.ntok > p.tt;
+            load_tiles(ld, cur, true, [&](int i) { return value_at(i, cur.hi - cur.lo, two); }, [] {});
         }
+        settle(ld);
+    } else if (wp == kQueryWarp) {
+        // --------------------------------------------------------- queries
+        few_regs();
+        uint32_t uses[2] = {0, 0};  // of row tile t so far
+        const uint32_t inv_g = 65536u / a.G + 1;  // r / G for r < 128
+        bool ok = true;
+        for (uint32_t s = 0; ok; ++s) {
+            ok = seg_wait(s);
+            if (!ok || sh.seg[s % kSegRing].tok0 < 0) break;
+            const Segment g = sh.seg[s % kSegRing];
+            seg_done(s);
+            const int nt = g.ntok > p.tt ? 2 : 1;
+            for (int t = 0; t < nt && ok; ++t) {
+                // the scores of the tile's last use are in
+                ok = warp_wait(&sh.q_free[t], (uses[t] & 1) ^ 1);
+                ++uses[t];
+                if (!ok) break;
+                uint8_t *dst = smem + t * C::kQBytes;
+                if (p.q_map) {
+                    // one box per 64 channels: G heads of tt tokens, in the order of
+                    // the tile's rows.  Rows past the item's (or the tile's) tokens
+                    // hold what is there: no row depends on another.
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sh.q_full[t], static_cast<uint32_t>(a.G * p.tt * 128 * NB));
+                        for (int cb = 0; cb < NB; ++cb)
+                            tma_load_3d(dst + cb * (kTile * 128), &p.tq, 64 * cb, g.h * a.G, g.tok0 + t * p.tt, &sh.q_full[t]);
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                // a layout that the map cannot describe: copies of 16 bytes
+                const int rows = min(p.tt, g.ntok - t * p.tt) * a.G;
+                const bf16 *q = a.q + (static_cast<int64_t>(g.tok0) + t * p.tt) * a.sq_t + static_cast<int64_t>(g.h) * a.G * a.sq_h;
+                constexpr int L = D / 8;  // lanes per row
+                const int ch = lane % L;
+                dst += (ch >> 3) * (kTile * 128);
+#pragma unroll 4
+                for (int r = lane / L; r < rows; r += 32 / L) {
+                    const int tok = static_cast<int>((r * inv_g) >> 16), hd = r - tok * a.G;
+                    cp_async16(dst + swz(r, ch & 7), q + tok * a.sq_t + hd * a.sq_h + 8 * ch, 16);
+                }
+                cp_async_wait_all();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full[t]);
+            }
+        }
+        if (!ok && lane == 0) fail();
+        // (a copy that is in flight when the warp gives up is one whose barrier the
+        // issuing warp waits for; let it land)
+        for (int t = 0; t < 2 && !ok; ++t)
+            if (uses[t] > 0) warp_wait(&sh.q_full[t], (uses[t] - 1) & 1);
     } else if (wp == kMmaWarp) {
         // ------------------------------------------- tensor cores: one thread
-        // The warp goes through the steps together and one elected thread issues:
-        // with elect.sync the compiler keeps descriptors and addresses in uniform
-        // registers, and a product of 16 keys costs 23 cycles to issue; under
-        // `lane == 0` it moves them there one by one, 54 cycles, which the 64
-        // cycles that the product takes do not hide once waits come between.
+        // One elected thread does it all.  With elect.sync the compiler keeps
+        // descriptors and addresses in uniform registers, and a product of 16 keys
+        // costs 23 cycles to issue; under `lane == 0` it moves them there one by
+        // one, 54 cycles, which the 64 cycles that the product takes do not hide
+        // once waits come between.  Waits, votes and elections by the whole warp
+        // cost another 350 of 2800 cycles per two tiles beside busy softmax warps.
         few_regs();
-        constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, false, !F16);
-        constexpr uint32_t kIdO = idesc_f16kind(kTile, D, false, true, !F16);
-        uint32_t taken = 0;                  // stages taken so far
-        uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
-        bool ok = true;
-        const uint32_t dq = desc_lo(sQ, 16);
-        auto stage = [&](uint32_t i) { return sRing + (i % C::kStages) * C::kStageBytes; };
-        auto wait_stage = [&](uint32_t i) { ok = ok && warp_wait(&full[i % C::kStages], (i / C::kStages) & 1); };
-        // S of stream x = Q K^T with row tile t; then the stage is free if `last`
-        auto scores = [&](int x, int t, uint32_t k, bool last) {
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t dk = desc_lo(stage(k), 16);
-            if (elect_one()) {
+        if (elect_one()) {
+            constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, false, !F16);
+            constexpr uint32_t kIdO = idesc_f16kind(kTile, D, false, true, !F16);
+            uint32_t taken = 0;                  // stages taken so far
+            uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+            bool ok = true;
+            const uint32_t dq = desc_lo(sQ, 16);
+            auto stage = [&](uint32_t i) { return sRing + (i % C::kStages) * C::kStageBytes; };
+            auto wait_stage = [&](uint32_t i) { ok = ok && mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1); };
+            // S of stream x = Q K^T with row tile t; then the stage is free if `last`, and
+        // the queries' tile if `q_last`
+            auto scores = [&](int x, int t, uint32_t k, bool last, bool q_last) {
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t dk = desc_lo(stage(k), 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     constexpr uint32_t kBlock = kTile * 128 / 16;  // 64 channels of a tile
                     const uint32_t step = (kk >> 2) * kBlock + (kk & 3) * 2;
                     mma_ss(tS(x), dq + t * (C::kQBytes / 16) + step, dk + step, kIdS, kk > 0);
                 }
-                mma_commit(&s_full[x]);
+                mma_commit(&sh.s_full[x]);
                 if (last) mma_commit(&empty[k % C::kStages]);
-            }
-            __syncwarp();
-        };
-        // O of stream x (+)= P V, each half of the keys as soon as its weights are
-        // in; then the stage is free if `free`, and the outputs complete if `done`
-        auto output = [&](int x, uint32_t v, bool first, bool free, bool done) {
-            const uint32_t dv = desc_lo(stage(v), kTile * 128);
-            ok = ok && warp_wait(&p_half[x], p_ph[x]);
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
+                if (q_last) mma_commit(&sh.q_free[t]);
+            };
+            // O of stream x (+)= P V, each half of the keys as soon as its weights are
+            // in; then the stage is free if `free`, and the outputs complete if `done`
+            auto output = [&](int x, uint32_t v, bool first, bool free, bool done) {
+                const uint32_t dv = desc_lo(stage(v), kTile * 128);
+                ok = ok && mbar_wait(&sh.p_half[x], p_ph[x]);
+                if (!ok) return;
+                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
                     mma_ts(tO(x), tS(x) + 8 * kk, dv + 128 * kk, kIdO, kk > 0 || !first);
-            }
-            __syncwarp();
-            ok = warp_wait(&p_full[x], p_ph[x]);
-            p_ph[x] ^= 1;
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
+                ok = mbar_wait(&sh.p_full[x], p_ph[x]);
+                p_ph[x] ^= 1;
+                if (!ok) return;
+                tc_fence_after();
 #pragma unroll
                 for (int kk = kTile / 32; kk < kTile / 16; ++kk)
                     mma_ts(tO(x), tS(x) + 8 * kk, dv + 128 * kk, kIdO, 1);
                 if (free) mma_commit(&empty[v % C::kStages]);
-                if (done) mma_commit(&o_full[x]);
-            }
-            __syncwarp();
-        };
-        auto wait_q = [&](int t) {
-            ok = ok && warp_wait(&q_full[t], q_ph[t]);
-            q_ph[t] ^= 1;
-        };
-        for (uint32_t s = 0; ok; ++s) {
-            ok = seg_wait(s);
-            if (!ok) break;
-            const Segment &g = s_seg[s % kSegRing];
-            if (g.tok0 < 0) break;
-            const int tiles = g.hi - g.lo;
-            const bool two = g.ntok > p.tt;
-            seg_done(s);
-            uint32_t k = taken++;
-            wait_stage(k);
-            wait_q(0);
-            scores(0, 0, k, !two);
-            if (two) {
-                wait_q(1);
-                scores(1, 1, k, true);
-                for (int i = 0; i < tiles && ok; ++i) {
-                    const uint32_t v = taken++;
-                    const bool more = i + 1 < tiles;
-                    if (more) k = taken++;
-                    wait_stage(v);
-                    output(0, v, i == 0, false, !more);
-                    if (more) {
-                        wait_stage(k);
-                        scores(0, 0, k, false);
+                if (done) mma_commit(&sh.o_full[x]);
+            };
+            auto wait_q = [&](int t) {
+                ok = ok && mbar_wait(&sh.q_full[t], q_ph[t]);
+                q_ph[t] ^= 1;
+            };
+            for (uint32_t s = 0; ok; ++s) {
+                ok = mbar_wait(&sh.seg_full[s % kSegRing], (s / kSegRing) & 1);
+                if (!ok) break;
+                const Segment &g = sh.seg[s % kSegRing];
+                if (g.tok0 < 0) break;
+                const int tiles = g.hi - g.lo;
+                const bool two = g.ntok > p.tt;
+                mbar_arrive(&sh.seg_empty[s % kSegRing]);
+                uint32_t k = taken++;
+                wait_stage(k);
+                wait_q(0);
+                scores(0, 0, k, !two, tiles == 1);
+                if (two) {
+                    wait_q(1);
+                    scores(1, 1, k, true, tiles == 1);
+                    for (int i = 0; i < tiles && ok; ++i) {
+                        const uint32_t v = taken++;
+                        const bool more = i + 1 < tiles;
+                        if (more) k = taken++;
+                        wait_stage(v);
+                        output(0, v, i == 0, false, !more);
+                        if (more) {
+                            wait_stage(k);
+                            scores(0, 0, k, false, i + 2 == tiles);
+                        }
+                        output(1, v, i == 0, true, !more);
+                        if (more) scores(1, 1, k, true, i + 2 == tiles);
                     }
-                    output(1, v, i == 0, true, !more);
-                    if (more) scores(1, 1, k, true);
-                }
-            } else {
-                if (tiles > 1) {
-                    k = taken++;
-                    wait_stage(k);
-                    scores(1, 0, k, true);
-                }
-                for (int i = 0; i < tiles && ok; ++i) {
-                    const uint32_t v = taken++;
-                    wait_stage(v);
-                    output(i & 1, v, i < 2, true, i + 2 >= tiles);
-                    if (i + 2 < tiles) {
+                } else {
+                    if (tiles > 1) {
                         k = taken++;
                         wait_stage(k);
-                        scores(i & 1, 0, k, true);
+                        scores(1, 0, k, true, tiles == 2);
+                    }
+                    for (int i = 0; i < tiles && ok; ++i) {
+                        const uint32_t v = taken++;
+                        wait_stage(v);
+                        output(i & 1, v, i < 2, true, i + 2 >= tiles);
+                        if (i + 2 < tiles) {
+                            k = taken++;
+                            wait_stage(k);
+                            scores(i & 1, 0, k, true, i + 3 == tiles);
+                        }
                     }
                 }
             }
+            // nothing may run on in Tensor Memory once it is released
+            mma_commit(&sh.drain);
+            if (!mbar_wait(&sh.drain, 0) || !ok) fail();
         }
-        if (!ok && lane == 0) fail();
-        // nothing may run on in Tensor Memory once it is released
-        if (elect_one()) mma_commit(&drain);
         __syncwarp();
-        if (!warp_wait(&drain, 0) && lane == 0) fail();
     } else if (wp < 8) {
         // ------------------------------------------- softmax: a thread per row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -706,41 +889,15 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        // queries of row tile t of a segment, by this group
-        auto load_q = [&](const Segment &g, int t) {
-            const int rows = min(p.tt, g.ntok - t * p.tt) * a.G;
-            const bf16 *q = a.q + (static_cast<int64_t>(g.tok0) + t * p.tt) * a.sq_t + static_cast<int64_t>(g.h) * a.G * a.sq_h;
-#pragma unroll 1
-            for (int i = 0; i < D / 8; ++i) {
-                const int at = row + 128 * i, r = at / (D / 8), ch = at % (D / 8);
-                const int tok = static_cast<int>((r * inv_g) >> 16), hd = r - tok * a.G;
-                const bool in = r < rows;
-                cp_async16(smem + t * C::kQBytes + (ch >> 3) * (kTile * 128) + swz(r, ch & 7),
-                           in ? q + tok * a.sq_t + hd * a.sq_h + 8 * ch : a.q, in ? 16 : 0);
-            }
-        };
-        auto q_ready = [&](bool t0, bool t1) {
-            if (!t0 && !t1) return;
-            cp_async_wait_all();
-            fence_proxy_async();
-            if (t0) arrive(&q_full[0]);
-            if (t1) arrive(&q_full[1]);
-        };
         bool ok = seg_wait(0);
         uint32_t steps = 0;              // tiles of this stream so far
         uint32_t o_ph[2] = {0, 0};       // segments in which stream 0, 1 had tiles
         uint32_t merges = 0;             // segments that were merged
-        if (ok && s_seg[0].tok0 >= 0) {
-            const bool t1 = x == 1 && s_seg[0].ntok > p.tt;
-            if (x == 0) load_q(s_seg[0], 0);
-            if (t1) load_q(s_seg[0], 1);
-            q_ready(x == 0, t1);
-        }
         // One segment; compiled once for two row tiles and once for one (a common
         // loop ran 8 % slower on the former).
         auto segment = [&](uint32_t s, auto two_tiles) {
             constexpr bool TWO = decltype(two_tiles)::value;
-            const Segment &g = s_seg[s % kSegRing], &ng = s_seg[(s + 1) % kSegRing];
+            const Segment &g = sh.seg[s % kSegRing];
             const int tiles = g.hi - g.lo;
             const bool merged = !TWO && tiles > 1;
             // the row's token in the segment, -1 if it has none
@@ -754,26 +911,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             constexpr int stride = TWO ? 1 : 2;
             const int begin = TWO ? 0 : x;
             float m = -INFINITY, l = 0.f;
-            // The next segment's queries, as soon as this segment's last scores
-            // are in: tile 0 by the group that sees them, tile 1 by group 1.
-            bool q0 = false, q1 = false;
-            auto next_q = [&]() {
-                ok = ok && seg_wait(s + 1);
-                if (!ok || ng.tok0 < 0) return;
-                q0 = TWO ? x == 0 : x == ((tiles - 1) & 1);
-                q1 = x == 1 && ng.ntok > p.tt;
-                if (q0) load_q(ng, 0);
-                if (q1) load_q(ng, 1);
-            };
-            if (begin >= tiles) next_q();
             // the first key of the tile, and the row's keys relative to it
             int lo = from - (g.lo + begin) * kTile, hi = upto - (g.lo + begin) * kTile;
             for (int i = begin; i < tiles && ok; i += stride, ++steps, lo -= stride * kTile, hi -= stride * kTile) {
-                ok = warp_wait(&s_full[x], steps & 1);
+                ok = warp_wait(&sh.s_full[x], steps & 1);
                 if (!ok) break;
-                if (i + stride >= tiles) next_q();
                 // group 1's outputs of the last merged segment have to be read
-                if (x == 1 && i == begin && merges > 0) ok = ok && warp_wait(&o_free, (merges - 1) & 1);
+                if (x == 1 && i == begin && merges > 0) ok = ok && warp_wait(&sh.o_free, (merges - 1) & 1);
                 if (!ok) break;
                 if (!idle) {
                     tc_fence_after();
@@ -784,7 +928,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
 #pragma unroll
                         for (int c = 0; c < 128; ++c)
-                            if (c < lo || c >= hi) u[c >> 5][c & 31] = 0xff800000u;
+                            if (c >= hi) u[c >> 5][c & 31] = 0xff800000u;
+                        if (a.window >= 0) {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c)
+                                if (c < lo) u[c >> 5][c & 31] = 0xff800000u;
+                        }
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -816,45 +965,69 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     }
                     const float base = m == -INFINITY ? 0.f : m * sl2;
                     const uint64_t scale2 = pair(sl2, sl2), base2 = pair(-base, -base);
-                    uint64_t sum2[2] = {0, 0};
+                    uint64_t sum2[4] = {0, 0, 0, 0};
+                    // The weights in groups of 8 scores, three of them under way: the
+                    // arguments of the next, the exponentials of this and the sums
+                    // and conversions of the last.  The order is written out (and
+                    // kept by `volatile`): left to the compiler, a tile took 1.6 k to
+                    // 2.1 k cycles alone and two tiles 2.1 k to 2.4 k on the same
+                    // schedulers, against 0.9 k and 1.3 k this way; the
+                    // special-function unit's own time is 0.5 k a tile.
+                    uint64_t arg[2][4];
+                    float ex[2][8] = {};
+                    uint32_t w[16];
+                    auto args = [&](int n) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 y = unpair(fma2(pair(__uint_as_float(u[c][2 * e]), __uint_as_float(u[c][2 * e + 1])), scale2, base2));
-                            const float a0 = ex2(y.x), a1 = ex2(y.y);
-                            sum2[e & 1] = add2(sum2[e & 1], pair(a0, a1));
-                            w[e] = F16 ? pack_f16_rn(a0, a1) : pack_bf2(a0, a1);
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = 8 * n + 2 * e;
+                            arg[n & 1][e] = fma2_here(pair(__uint_as_float(u[c >> 5][c & 31]), __uint_as_float(u[c >> 5][(c & 31) + 1])), scale2, base2);
                         }
-                        tmem_st16(tS(x) + lanes + 16 * c, w);
-                        if (c == 1) {  // the first half of the keys: their product may begin
+                    };
+                    auto finish = [&](int n, int e) {
+                        const float a0 = ex[n & 1][2 * e], a1 = ex[n & 1][2 * e + 1];
+                        sum2[e] = add2(sum2[e], pair(a0, a1));
+                        w[4 * (n & 3) + e] = F16 ? pack_f16_rn(a0, a1) : pack_bf2(a0, a1);
+                    };
+                    args(0);
+#pragma unroll
+                    for (int n = 0; n <= 16; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (n < 16) {
+                                const float2 z = unpair(arg[n & 1][e]);
+                                ex[n & 1][2 * e] = ex2_here(z.x);
+                                if (e == 1 && n < 15) args(n + 1);
+                                ex[n & 1][2 * e + 1] = ex2_here(z.y);
+                            }
+                            if (n > 0) finish(n - 1, e);
+                        }
+                        if (n > 0 && n % 4 == 0) tmem_st16(tS(x) + lanes + 4 * (n - 4), w);
+                        if (n == 9) {  // the first half of the keys: their product may begin
                             tmem_st_wait();
                             tc_fence_before();
-                            arrive(&p_half[x]);
+                            arrive(&sh.p_half[x]);
                         }
                     }
-                    const float2 t = unpair(add2(sum2[0], sum2[1]));
+                    const float2 t = unpair(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
                     l += t.x + t.y;
                     tmem_st_wait();
                     tc_fence_before();
                 } else {
-                    arrive(&p_half[x]);
+                    arrive(&sh.p_half[x]);
                 }
-                arrive(&p_full[x]);
+                arrive(&sh.p_full[x]);
             }
             if (!ok) return;
-            q_ready(q0, q1);
             if (merged && x == 1) {  // group 0 merges
-                s_ml[row] = make_float2(m, l);
-                arrive(&ml_full);
+                sh.ml[row] = make_float2(m, l);
+                arrive(&sh.ml_full);
             }
             if (TWO || x == 0) {
-                ok = warp_wait(&o_full[x], o_ph[x] & 1);
+                ok = warp_wait(&sh.o_full[x], o_ph[x] & 1);
                 float f0 = 1.f, f1 = 0.f;
                 if (merged) {
-                    ok = ok && warp_wait(&o_full[1], o_ph[1] & 1) && warp_wait(&ml_full, merges & 1);
-                    const float2 ml = s_ml[row];
+                    ok = ok && warp_wait(&sh.o_full[1], o_ph[1] & 1) && warp_wait(&sh.ml_full, merges & 1);
+                    const float2 ml = sh.ml[row];
                     const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top * sl2;
                     f0 = ex2(fmaf(m, sl2, -base));
                     f1 = ex2(fmaf(ml.x, sl2, -base));
@@ -866,63 +1039,98 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                 if (!idle) {
                     const bool whole = g.slot < 0;
                     const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                    const int head = g.h * a.G + my_head;
-                    const int64_t tok_row = static_cast<int64_t>(g.tok0) + max(tok, 0);
-                    bf16 *o = a.out + tok_row * a.so_t + head * a.so_h;
-                    const int64_t part = static_cast<int64_t>(max(g.slot, 0)) * 2 * kTile + tile * kTile + row;
-                    float *po = p.part_o + part * D;
                     f0 *= inv;
                     f1 *= inv;
+                    if (tok >= 0) {
+                        const int64_t at = static_cast<int64_t>(g.tok0) + tok;
+                        const float base = m == -INFINITY ? -INFINITY : m * sl2;
+                        if (!whole)
+                            p.part_ml[static_cast<int64_t>(g.slot) * 2 * kTile + tile * kTile + row] = make_float2(base, l);
+                        else if (a.lse)
+                            a.lse[at * a.HQ + g.h * a.G + my_head] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+                    }
+                    // The rows out: the outputs are read in the shape of 16 lanes, a
+                    // quad of threads per row, and exchanged within the quad so that
+                    // it stores 64 consecutive bytes of the row (16 per thread): a
+                    // store then touches 8 lines instead of the 32 of a thread per
+                    // row, which took 4 k cycles an item.
+                    const int q = lane & 3;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        __syncwarp();
-                        uint32_t u[32];
-                        tmem_ld32(tO(x) + lanes + c, u);
-                        tmem_ld_wait();
-                        if (merged) {
-                            uint32_t v[32];
-                            tmem_ld32(tO(1) + lanes + c, v);
-                            tmem_ld_wait();
+                    for (int half = 0; half < 2; ++half) {
+                        float g0[2], g1[2];
+                        bf16 *o[2];
+                        float *po[2];
+                        bool in[2];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                u[e] = __float_as_uint(__uint_as_float(u[e]) * f0 + __uint_as_float(v[e]) * f1);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f0);
+                        for (int h = 0; h < 2; ++h) {
+                            const int src = 16 * half + 8 * h + (lane >> 2);  // the thread that has the row
+                            g0[h] = __shfl_sync(0xffffffffu, f0, src);
+                            g1[h] = __shfl_sync(0xffffffffu, f1, src);
+                            const int t = __shfl_sync(0xffffffffu, tok, src), hd = __shfl_sync(0xffffffffu, my_head, src);
+                            in[h] = t >= 0;
+                            o[h] = a.out + (static_cast<int64_t>(g.tok0) + max(t, 0)) * a.so_t + static_cast<int64_t>(g.h * a.G + hd) * a.so_h;
+                            po[h] = p.part_o + (static_cast<int64_t>(max(g.slot, 0)) * 2 * kTile + tile * kTile + 32 * (wp & 3) + src) * D;
                         }
-                        if (tok < 0) continue;
-                        if (whole) {
+                        const uint32_t at = lanes + (static_cast<uint32_t>(16 * half) << 16);
+                        uint32_t all[D / 64][32];  // [c / 64][4 n + 2 h + e]: row h, column c + 8 n + 2 q + e
+                        __syncwarp();
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint32_t w[4];
+                        for (int c = 0; c < D; c += 64) tmem_ld_rows(tO(x) + at + c, all[c / 64]);
+                        tmem_ld_wait();
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const float y = __uint_as_float(u[e + 2 * k]), z = __uint_as_float(u[e + 2 * k + 1]);
-                                    w[k] = F16 ? pack_f16_rn(y, z) : pack_bf2(y, z);
-                                }
-                                *reinterpret_cast<uint4 *>(o + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int c = 0; c < D; c += 64) {
+                            uint32_t(&u)[32] = all[c / 64];
+                            if (merged) {
+                                uint32_t v[32];
+                                tmem_ld_rows(tO(1) + at + c, v);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    u[e] = __float_as_uint(__uint_as_float(u[e]) * g0[(e >> 1) & 1] + __uint_as_float(v[e]) * g1[(e >> 1) & 1]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * g0[(e >> 1) & 1]);
                             }
-                        } else {
+                            if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4 *>(po + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                                for (int n = 0; n < 8; n += 4)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        uint32_t w[4];  // columns 8 (n + k) + 2 q, + 1
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k) {
+                                            const float y0 = __uint_as_float(u[4 * (n + k) + 2 * h]), y1 = __uint_as_float(u[4 * (n + k) + 2 * h + 1]);
+                                            w[k] = F16 ? pack_f16_rn(y0, y1) : pack_bf2(y0, y1);
+                                        }
+                                        quad_transpose(w, q);
+                                        if (in[h]) *reinterpret_cast<uint4 *>(o[h] + c + 8 * (n + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+                                    }
+                            } else {
+#pragma unroll
+                                for (int n = 0; n < 8; n += 2)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        // an even thread keeps group n, an odd one group n + 1
+                                        const bool odd = q & 1;
+                                        const uint32_t a0 = u[4 * n + 2 * h], a1 = u[4 * n + 2 * h + 1], b0 = u[4 * n + 4 + 2 * h], b1 = u[4 * n + 5 + 2 * h];
+                                        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, odd ? a0 : b0, 1), r1 = __shfl_xor_sync(0xffffffffu, odd ? a1 : b1, 1);
+                                        if (in[h])
+                                            *reinterpret_cast<uint4 *>(po[h] + c + 8 * (n + (q & 1)) + 2 * (q & 2)) =
+                                                odd ? make_uint4(r0, r1, b0, b1) : make_uint4(a0, a1, r0, r1);
+                                    }
+                            }
                         }
                     }
-                    const float base = m == -INFINITY ? -INFINITY : m * sl2;
-                    if (tok >= 0 && !whole)
-                        p.part_ml[part] = make_float2(base, l);
-                    else if (tok >= 0 && a.lse)
-                        a.lse[tok_row * a.HQ + head] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
                 }
                 tc_fence_before();
-                if (merged) arrive(&o_free);
+                if (merged) arrive(&sh.o_free);
             }
             o_ph[0] += 1;
             o_ph[1] += TWO || merged;
             merges += merged;
         };
         for (uint32_t s = 0; ok; ++s) {
-            const Segment &g = s_seg[s % kSegRing];
+            const Segment &g = sh.seg[s % kSegRing];
             if (g.tok0 < 0) break;
             if (g.ntok > p.tt)
                 segment(s, std::true_type());
@@ -933,16 +1141,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             ok = ok && seg_wait(s + 1);
         }
         if (!ok) fail();
-        cp_async_wait_all();
-    } else {
-        few_regs();
     }
     __syncthreads();
     if (wp == kMmaWarp) {
         tmem_relinquish();
         tmem_dealloc(tm, 512);
     }
-    if (tid == 0) p.flags[blockIdx.x] = s_share.flags;
+    if (tid == 0) p.flags[blockIdx.x] = sh.share.flags;
 }
 
 // ---------------------------------------------------------------- combine
@@ -1065,7 +1270,21 @@ bool encode_cache(CUtensorMap *map, int (&pos)[3], const void *base, const AttnP
     }
     return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor map over the queries [T, HQ, D]: a box is G heads of `tt` tokens and 64
+// channels.  False where the driver rejects the layout (or a stride is zero).
+bool encode_queries(CUtensorMap *map, const AttnParams &a, int D, bool f16, int tt) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc || (a.HQ > 1 && a.sq_h == 0) || (a.T > 1 && a.sq_t == 0)) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.HQ), static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>((a.HQ > 1 ? a.sq_h : D) * 2),
+                                   static_cast<cuuint64_t>((a.T > 1 ? a.sq_t : D) * 2)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(tt)}, estr[3] = {1, 1, 1};
+    return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(a.q),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, bool F16>
@@ -1101,6 +1320,7 @@ cudaError_t launch_paged_attn(const AttnParams &a, const gdn2_attn_dims &d, int 
     if (a.T > 0 && (!encode_cache(&p.tk, p.kpos, a.k_cache, a, a.skc, d.D, f16, p.granule) ||
                     !encode_cache(&p.tv, p.vpos, a.v_cache, a, a.svc, d.D, f16, p.granule)))
         return cudaErrorInvalidValue;
+    p.q_map = a.T > 0 && encode_queries(&p.tq, a, d.D, f16, p.tt);
     if (d.D == 64) return f16 ? launch<64, true>(p, ctas, s) : launch<64, false>(p, ctas, s);
     return f16 ? launch<128, true>(p, ctas, s) : launch<128, false>(p, ctas, s);
 }
