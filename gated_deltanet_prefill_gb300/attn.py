@@ -9,6 +9,7 @@ does not pass them, and there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -92,75 +93,114 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, trained_
     return f.to(device), rope_factor
 
 
-def _code(ref, *tensors):
+# A decode step calls these functions with a few microseconds of GPU work per call,
+# so what depends on the tensors' metadata alone (the checks, the dims struct, the
+# workspace size) is worked out once per set of shapes, strides and dtypes and kept
+# (`_norm_rope_plan` and its like, keyed by that metadata); a call then costs its
+# allocations and the library's launch.  Nothing is kept by address or content.
+_PLANS = 512
+
+
+def _rows(t):
+    """Metadata of a strided tensor."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.is_cuda)
+
+
+def _flat(t):
+    """Metadata of a tensor that has to be contiguous."""
+    return None if t is None else (t.numel(), t.dtype, t.is_cuda and t.is_contiguous())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    def _stream(t, stream):
+        return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream
+else:
+    def _stream(t, stream):
+        return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+
+
+def _code(*metas):
     """dtype code of the call: the tensors' one 16-bit dtype (99: refused by the library)."""
-    for t in tensors:
-        if t is not None and t.dtype != ref.dtype:
-            return 99
-    return _DTYPE_CODE.get(ref.dtype, 99)
+    dtypes = {m[2] for m in metas if m is not None}
+    return _DTYPE_CODE.get(dtypes.pop(), 99) if len(dtypes) == 1 else 99
 
 
-def _rows(name, t):
+def _check_rows(name, m, shape=None):
     """(token, head) strides of a [T, heads, D] tensor on the device."""
-    if not t.is_cuda:
+    size, stride, _, cuda = m
+    if not cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    s = t.stride()
-    if len(s) != 3 or s[2] != 1:
+    if len(size) != 3 or stride[2] != 1:
         raise ValueError("%s must be [tokens, heads, channels] with contiguous channels" % name)
-    return s[:2]
-
-
-def _same_shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and tuple(size) != tuple(shape):
         raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    return stride[:2]
 
 
-def _flat(name, t, dtypes, n=None):
-    """A contiguous device tensor of one of the dtypes, with n elements."""
-    if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous() or (n is not None and t.numel() != n):
+def _check_flat(name, m, dtypes, n=None):
+    if not m[2] or m[1] not in dtypes or (n is not None and m[0] != n):
         raise ValueError("%s must be a contiguous CUDA tensor of %s%s" % (
             name, " or ".join(str(d) for d in dtypes), "" if n is None else " with %d elements" % n))
-    return t.data_ptr()
 
 
-def _weights(norm, D, ref, q_weight, k_weight):
-    if not norm and (q_weight is not None or k_weight is not None):
-        raise ValueError("a norm weight was given, but norm is off")
-    return [None if w is None else _flat("norm weight", w, (ref.dtype,), D) for w in (q_weight, k_weight)]
-
-
-def _rotation(inv_freq, positions, T, need_positions):
-    """(rot_dim, inv_freq pointer, positions pointer, positions are int64)."""
+def _check_rope(norm, ref, D, T, q_weight, k_weight, inv_freq, positions, need_positions):
+    """(rot_dim, positions are int64)."""
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if not norm:
+                raise ValueError("a norm weight was given, but norm is off")
+            _check_flat("norm weight", w, (ref[2],), D)
     if inv_freq is None:
-        return 0, None, None, 0
-    f = _flat("inv_freq", inv_freq, (torch.float64,))
+        return 0, 0
+    _check_flat("inv_freq", inv_freq, (torch.float64,))
     if positions is None:
         if need_positions:
             raise ValueError("positions are required with inv_freq")
-        return 2 * inv_freq.numel(), f, None, 0
-    p = _flat("positions", positions, (torch.int32, torch.int64), T)
-    return 2 * inv_freq.numel(), f, p, 1 if positions.dtype == torch.int64 else 0
+        return 2 * inv_freq[0], 0
+    _check_flat("positions", positions, (torch.int32, torch.int64), T)
+    return 2 * inv_freq[0], 1 if positions[1] == torch.int64 else 0
 
 
-def _paged(k_cache, v_cache, block_table, kv_lens, cu_seqlens):
-    """Shapes, strides and pointers of the cache and its tables."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or not k_cache.is_cuda or not v_cache.is_cuda:
+def _check_paged(k_cache, v_cache, table, lens, cu):
+    """(sequences, strides of k_cache and v_cache, row stride and width of the table, cu is int64)."""
+    if len(k_cache[0]) != 4 or k_cache[0] != v_cache[0] or not k_cache[3] or not v_cache[3]:
         raise ValueError("k_cache and v_cache must be CUDA tensors [pages, page_size, heads, channels] of one shape")
-    kc, vc = k_cache.stride(), v_cache.stride()
+    kc, vc = k_cache[1], v_cache[1]
     if kc[3] != 1 or vc[3] != 1:
         raise ValueError("k_cache and v_cache: channels must be contiguous")
-    n = cu_seqlens.numel() - 1
-    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 \
-            or block_table.shape[0] != n or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    n = cu[0] - 1
+    size, stride, dtype, cuda = table
+    if not cuda or dtype != torch.int32 or len(size) != 2 or size[0] != n or (size[1] > 1 and stride[1] != 1):
         raise ValueError("block_table must be an int32 CUDA tensor [sequences, pages] with contiguous rows")
-    cu = _flat("cu_seqlens", cu_seqlens, (torch.int32, torch.int64))
-    lens = _flat("kv_lens", kv_lens, (torch.int32,), n)
-    width = block_table.shape[1]
-    return n, kc[:3], vc[:3], max(block_table.stride(0), width), width, cu, lens
+    _check_flat("cu_seqlens", cu, (torch.int32, torch.int64))
+    _check_flat("kv_lens", lens, (torch.int32,), n)
+    return n, kc[:3], vc[:3], max(stride[0], size[1]), size[1], 1 if cu[1] == torch.int64 else 0
 
 
-def _stream(t, stream):
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+@functools.lru_cache(maxsize=_PLANS)
+def _norm_rope_plan(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions, norm, interleaved, eps, rope_factor):
+    if len(q[0]) != 3:
+        raise ValueError("q must be [tokens, heads, channels]")
+    T, HQ, D = q[0]
+    qs = _check_rows("q", q)
+    qo = (HQ * D, D) if q_out is None else _check_rows("q_out", q_out, (T, HQ, D))
+    HK, ks, ko = 0, (0, 0), (0, 0)
+    if k is not None:
+        ks = _check_rows("k", k)
+        HK = k[0][1]
+        _check_rows("k", k, (T, HK, D))
+        ko = (HK * D, D) if k_out is None else _check_rows("k_out", k_out, (T, HK, D))
+    elif k_out is not None:
+        raise ValueError("k_out was given without k")
+    rot, pos64 = _check_rope(norm, q, D, T, q_weight, k_weight, inv_freq, positions, True)
+    dims = AttnDims(T, 0, qs, ks, (0, 0), qo, ko, (0, 0, 0), (0, 0, 0), 0, 0, HQ, HK, D, 0, 0,
+                    _code(q, k, q_out, k_out), 0, pos64, 1 if norm else 0, rot, 1 if interleaved else 0, 1, -1, eps,
+                    rope_factor)
+    return ctypes.byref(dims), (T, HQ, D), (T, HK, D)
 
 
 def qk_norm_rope(q, k=None, positions=None, inv_freq=None, rope_factor=1.0, interleaved=False, norm=True,
@@ -177,30 +217,43 @@ def qk_norm_rope(q, k=None, positions=None, inv_freq=None, rope_factor=1.0, inte
     k_out).
     """
     lib = load()
-    T, HQ, D = q.shape
-    HK = 0
-    if k is not None:
-        HK = k.shape[1]
-        _same_shape("k", k, (T, HK, D))
-    q_out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    _same_shape("q_out", q_out, (T, HQ, D))
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out was given without k")
-    else:
-        k_out = torch.empty((T, HK, D), dtype=k.dtype, device=k.device) if k_out is None else k_out
-        _same_shape("k_out", k_out, (T, HK, D))
-    wq, wk = _weights(norm, D, q, q_weight, k_weight)
-    rot, f, pos, pos64 = _rotation(inv_freq, positions, T, True)
-    ks, kos = (_rows("k", k), _rows("k_out", k_out)) if k is not None else ((0, 0), (0, 0))
-    dims = AttnDims(T, 0, _rows("q", q), ks, (0, 0), _rows("q_out", q_out), kos, (0, 0, 0), (0, 0, 0), 0, 0, HQ, HK,
-                    D, 0, 0, _code(q, k, q_out, k_out), 0, pos64, 1 if norm else 0, rot, 1 if interleaved else 0, 1,
-                    -1, eps, rope_factor)
-    st = lib.gdn2_qk_norm_rope(q.data_ptr(), None if k is None else k.data_ptr(), wq, wk, f, pos, q_out.data_ptr(),
-                               None if k is None else k_out.data_ptr(), dims, _stream(q, stream))
+    dims, q_shape, k_shape = _norm_rope_plan(_rows(q), _rows(k), _rows(q_out), _rows(k_out), _flat(q_weight),
+                                             _flat(k_weight), _flat(inv_freq), _flat(positions), bool(norm),
+                                             bool(interleaved), eps, rope_factor)
+    if q_out is None:
+        q_out = torch.empty(q_shape, dtype=q.dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k_shape, dtype=k.dtype, device=k.device)
+    st = lib.gdn2_qk_norm_rope(q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                               _ptr(positions), q_out.data_ptr(), _ptr(k_out), dims, _stream(q, stream))
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_qk_norm_rope")
     return q_out, k_out
+
+
+@functools.lru_cache(maxsize=_PLANS)
+def _append_plan(q, k, v, q_out, k_cache, v_cache, table, lens, cu, q_weight, k_weight, inv_freq, positions, norm,
+                 interleaved, eps, rope_factor):
+    ks = _check_rows("k", k)
+    T, HKV, D = k[0]
+    vs = _check_rows("v", v, (T, HKV, D))
+    n, kc, vc, ts, width, cu64 = _check_paged(k_cache, v_cache, table, lens, cu)
+    pages, page = k_cache[0][:2]
+    if tuple(k_cache[0]) != (pages, page, HKV, D):
+        raise ValueError("k_cache must have shape %s" % ((pages, page, HKV, D),))
+    HQ, qs, qo = 0, (0, 0), (0, 0)
+    if q is not None:
+        qs = _check_rows("q", q)
+        HQ = q[0][1]
+        _check_rows("q", q, (T, HQ, D))
+        qo = (HQ * D, D) if q_out is None else _check_rows("q_out", q_out, (T, HQ, D))
+    elif q_out is not None:
+        raise ValueError("q_out was given without q")
+    rot, pos64 = _check_rope(norm, k, D, T, q_weight, k_weight, inv_freq, positions, False)
+    dims = AttnDims(T, pages, qs, ks, vs, qo, (0, 0), kc, vc, ts, n, HQ, HKV, D, page, width,
+                    _code(k, v, q, q_out, k_cache, v_cache), cu64, pos64, 1 if norm else 0, rot,
+                    1 if interleaved else 0, 1, -1, eps, rope_factor)
+    return ctypes.byref(dims), (T, HQ, D)
 
 
 def append_kv(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q=None, positions=None, inv_freq=None,
@@ -219,33 +272,38 @@ def append_kv(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q=None, 
     (None without q).
     """
     lib = load()
-    T, HKV, D = k.shape
-    _same_shape("v", v, (T, HKV, D))
-    n, kc, vc, ts, width, cu, lens = _paged(k_cache, v_cache, block_table, kv_lens, cu_seqlens)
-    pages, page = k_cache.shape[:2]
-    _same_shape("k_cache", k_cache, (pages, page, HKV, D))
-    HQ, qs, qos = 0, (0, 0), (0, 0)
-    if q is not None:
-        HQ = q.shape[1]
-        _same_shape("q", q, (T, HQ, D))
-        q_out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _same_shape("q_out", q_out, (T, HQ, D))
-        qs, qos = _rows("q", q), _rows("q_out", q_out)
-    elif q_out is not None:
-        raise ValueError("q_out was given without q")
-    wq, wk = _weights(norm, D, k, q_weight, k_weight)
-    rot, f, pos, pos64 = _rotation(inv_freq, positions, T, False)
+    dims, q_shape = _append_plan(_rows(q), _rows(k), _rows(v), _rows(q_out), _rows(k_cache), _rows(v_cache),
+                                 _rows(block_table), _flat(kv_lens), _flat(cu_seqlens), _flat(q_weight),
+                                 _flat(k_weight), _flat(inv_freq), _flat(positions), bool(norm), bool(interleaved),
+                                 eps, rope_factor)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q_shape, dtype=q.dtype, device=q.device)
     if workspace is None:
         workspace = torch.empty(64, dtype=torch.uint8, device=k.device)
-    dims = AttnDims(T, pages, qs, _rows("k", k), _rows("v", v), qos, (0, 0), kc, vc, ts, n, HQ, HKV, D, page, width,
-                    _code(k, v, q, q_out, k_cache, v_cache), 1 if cu_seqlens.dtype == torch.int64 else 0, pos64,
-                    1 if norm else 0, rot, 1 if interleaved else 0, 1, -1, eps, rope_factor)
-    st = lib.gdn2_kv_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), wq, wk, f, pos, cu, lens,
-                            block_table.data_ptr(), None if q is None else q_out.data_ptr(), k_cache.data_ptr(),
-                            v_cache.data_ptr(), dims, workspace.data_ptr(), workspace.numel(), _stream(k, stream))
+    st = lib.gdn2_kv_append(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                            _ptr(positions), cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
+                            _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), dims, workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), _stream(k, stream))
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_kv_append")
     return q_out
+
+
+@functools.lru_cache(maxsize=_PLANS)
+def _attn_plan(q, k_cache, v_cache, table, lens, cu, out, lse, causal, window_left):
+    qs = _check_rows("q", q)
+    T, HQ, D = q[0]
+    n, kc, vc, ts, width, cu64 = _check_paged(k_cache, v_cache, table, lens, cu)
+    pages, page, HKV, dk = k_cache[0]
+    if dk != D:
+        raise ValueError("the cache's channels differ from q's")
+    os = (HQ * D, D) if out is None else _check_rows("out", out, (T, HQ, D))
+    if lse is not None:
+        _check_flat("lse", lse, (torch.float32,), T * HQ)
+    dims = AttnDims(T, pages, qs, (0, 0), (0, 0), os, (0, 0), kc, vc, ts, n, HQ, HKV, D, page, width,
+                    _code(q, out, k_cache, v_cache), cu64, 0, 0, 0, 0, 1 if causal else 0, window_left, 0.0, 1.0)
+    ref = ctypes.byref(dims)
+    return ref, (T, HQ, D), (T, HQ), max(load().gdn2_paged_attn_workspace_bytes(ref), 64)
 
 
 def paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale=None, causal=True, window_left=-1,
@@ -260,25 +318,19 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale=
     ``return_lse``; a token with no key gets zeros and lse -inf.
     """
     lib = load()
-    T, HQ, D = q.shape
-    n, kc, vc, ts, width, cu, lens = _paged(k_cache, v_cache, block_table, kv_lens, cu_seqlens)
-    pages, page, HKV, dk = k_cache.shape
-    if dk != D:
-        raise ValueError("the cache's channels differ from q's")
-    out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device) if out is None else out
-    _same_shape("out", out, (T, HQ, D))
-    if lse is None:
-        lse = torch.empty((T, HQ), dtype=torch.float32, device=q.device) if return_lse else None
-    lse_ptr = None if lse is None else _flat("lse", lse, (torch.float32,), T * HQ)
-    dims = AttnDims(T, pages, _rows("q", q), (0, 0), (0, 0), _rows("out", out), (0, 0), kc, vc, ts, n, HQ, HKV, D,
-                    page, width, _code(q, out, k_cache, v_cache), 1 if cu_seqlens.dtype == torch.int64 else 0, 0, 0,
-                    0, 0, 1 if causal else 0, window_left, 0.0, 1.0)
+    dims, shape, lse_shape, need = _attn_plan(_rows(q), _rows(k_cache), _rows(v_cache), _rows(block_table),
+                                              _flat(kv_lens), _flat(cu_seqlens), _rows(out), _flat(lse), bool(causal),
+                                              window_left)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
     if workspace is None:
-        need = lib.gdn2_paged_attn_workspace_bytes(dims)
-        workspace = torch.empty(max(need, 64), dtype=torch.uint8, device=q.device)
-    st = lib.gdn2_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cu, lens,
-                                 block_table.data_ptr(), 0.0 if scale is None else scale, out.data_ptr(), lse_ptr,
-                                 dims, workspace.data_ptr(), workspace.numel(), _stream(q, stream))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = lib.gdn2_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens.data_ptr(),
+                                 kv_lens.data_ptr(), block_table.data_ptr(), 0.0 if scale is None else scale,
+                                 out.data_ptr(), _ptr(lse), dims, workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(q, stream))
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_paged_attn_fwd")
     return (out, lse) if return_lse else out
