@@ -125,23 +125,26 @@ __device__ __forceinline__ int item_cost(const AttnParams &a, int len, int fresh
     return max(1, s.hi - s.lo);
 }
 
-// sum over i < n of floor((a i + b) / 128), a, b >= 0.
-__device__ long long floor_sum(long long n, long long a, long long b) {
-    long long m = 128, sum = 0;
+// sum over i < n of floor((a i + b) / 128); a n + b < 2^32.
+__device__ long long floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+    uint32_t m = 128;
+    long long sum = 0;
     while (n > 0) {
         if (a >= m) {
-            sum += (n - 1) * n / 2 * (a / m);
-            a %= m;
+            const uint32_t q = a / m;
+            sum += static_cast<long long>(n - 1) * n / 2 * q;
+            a -= q * m;
         }
         if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
+            const uint32_t q = b / m;
+            sum += static_cast<long long>(n) * q;
+            b -= q * m;
         }
-        const long long top = a * n + b;
+        const uint32_t top = a * n + b;
         if (top < m) break;
         n = top / m;
-        b = top % m;
-        const long long t = m;
+        b = top - n * m;
+        const uint32_t t = m;
         m = a;
         a = t;
     }
@@ -157,7 +160,7 @@ __device__ long long cost_of(const AttnParams &a, int len, int fresh, int tokens
     if (!a.causal) return static_cast<long long>(items) * max(1, (len + kTile - 1) / kTile);
     // item m: ceil((len - fresh + min(fresh, (m + 1) tokens)) / 128); the last one apart
     const long long last = (len - fresh + min(static_cast<long long>(fresh), static_cast<long long>(items) * tokens) + kTile - 1) / kTile;
-    return last + floor_sum(items - 1, tokens, static_cast<long long>(len) - fresh + tokens + kTile - 1);
+    return last + floor_sum(items - 1, tokens, static_cast<uint32_t>(len - fresh) + tokens + kTile - 1);
 }
 
 __device__ __forceinline__ long long div_by(long long x, long long y) {
@@ -185,10 +188,9 @@ __device__ __forceinline__ Seq seq_at(const AttnParams &a, int n, int *flags) {
     return q;
 }
 
-// Cost of the sequence n = base + threadIdx.x per key head; called by whole warps.
-__device__ long long seq_cost(const AttnParams &a, int n, int tokens, int *flags) {
+// Cost of a sequence per key head; called by whole warps, a sequence per lane.
+__device__ long long seq_cost(const AttnParams &a, const Seq &q, int tokens) {
     const int lane = threadIdx.x & 31;
-    const Seq q = seq_at(a, n, flags);
     long long cost = q.fresh == 0 ? 0 : q.fresh <= tokens ? item_cost(a, q.len, q.fresh, tokens, 0)
                      : closed_form(a, q.len, q.fresh) ? cost_of(a, q.len, q.fresh, tokens, (q.fresh + tokens - 1) / tokens)
                                                       : -1;
@@ -208,64 +210,72 @@ struct Share {
     long long total, shares;
     long long in_seq, cost;  // offset of the first tile in its sequence, the sequence's cost per head
     int n, flags;            // sequence of the first tile
+    Seq q;
     long long part[kThreads / 32];
 };
 
-// The share of this CTA; every thread of the block calls it, s is in shared memory.
+// The share of this CTA; every thread of the block calls it, s is in shared memory
+// (flags and left zero).
 __device__ void find_share(const AttnParams &a, int tokens, Share &s) {
-    long long *const part = s.part;
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
     int flags = 0;
-    if (tid == 0) {
-        s.flags = 0;
-        s.left = 0;
-        if (a.N > 0 ? cu_of(a.cu, a.cu64, 0) != 0 || cu_of(a.cu, a.cu64, a.N) != a.T : a.T != 0) flags = kBadCu;
-    }
-    long long sum = 0, first = 0;
-    for (int base = 0; base < a.N; base += kThreads) {
-        const long long c = seq_cost(a, base + tid, tokens, &flags);
-        if (base == 0) first = c;
-        sum += c;
-    }
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) part[wp] = sum;
-    __syncthreads();
-    if (flags) atomicOr(&s.flags, flags);
-    long long total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) total += part[i];
-    total *= a.HKV;
-    __syncthreads();
-    if (s.flags || total == 0) return;
-    const long long shares = min(total, static_cast<long long>(gridDim.x));
-    if (blockIdx.x >= shares) return;
-    const long long begin = div_by(total * blockIdx.x, shares), end = div_by(total * (blockIdx.x + 1), shares);
-    long long done = 0;  // tiles of the sequences before the round
-    for (int base = 0; base < a.N; base += kThreads) {
-        const long long c = base == 0 ? first : seq_cost(a, base + tid, tokens, nullptr);
+    if (tid == 0 && (a.N > 0 ? cu_of(a.cu, a.cu64, 0) != 0 || cu_of(a.cu, a.cu64, a.N) != a.T : a.T != 0)) flags = kBadCu;
+    // cost of the sequence, and its inclusive sum over the warp
+    auto scan = [&](int n, Seq &q, long long &c, int *f) {
+        q = seq_at(a, n, f);
+        c = seq_cost(a, q, tokens);
         long long x = c;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) part[wp] = x;
+        return x;
+    };
+    Seq q;
+    long long c, x, total = 0, before = 0;
+    for (int base = 0; base < a.N || base == 0; base += kThreads) {  // the rounds before the last only add up
+        x = scan(base + tid, q, c, &flags);
+        if (lane == 31) s.part[wp] = x;
+        if (flags) atomicOr(&s.flags, flags);
         __syncthreads();
-        long long before = done;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            if (i < wp) before += part[i];
-            done += part[i];
+        before = total;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) total += s.part[i];
+        if (base + kThreads < a.N) __syncthreads();
+    }
+    const bool one_round = a.N <= kThreads;
+    total *= a.HKV;
+    if (s.flags || total == 0) return;
+    const long long shares = min(total, static_cast<long long>(gridDim.x));
+    if (blockIdx.x >= shares) return;
+    const long long begin = div_by(total * blockIdx.x, shares), end = div_by(total * (blockIdx.x + 1), shares);
+    before = 0;
+    for (int base = 0; base < a.N; base += kThreads) {
+        if (!one_round) {
+            __syncthreads();
+            x = scan(base + tid, q, c, nullptr);
+            if (lane == 31) s.part[wp] = x;
+            __syncthreads();
         }
-        const long long from = (before + x - c) * a.HKV;
+        long long from = before;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < wp) from += s.part[i];
+            before += s.part[i];
+        }
+        from = (from + x - c) * a.HKV;
         if (begin >= from && begin < from + c * a.HKV) {
             s.begin = begin;
             s.left = end - begin;
             s.total = total;
             s.shares = shares;
             s.n = base + tid;
+            s.q = q;
             s.in_seq = begin - from;
             s.cost = c;
         }
-        __syncthreads();
-        if (done * a.HKV > begin) break;
+        if (before * a.HKV > begin) break;
     }
 }
 
@@ -277,18 +287,29 @@ struct Walk {
     int items;              // row-tile groups of the sequence
     long long left;
     bool first;
-    Seq q, ahead;           // this sequence, and the next one's loaded ahead
+    Seq q;                  // this sequence
+    int64_t end_ahead;      // and the next one's numbers, read ahead
+    int len_ahead;
+
+    __device__ void read_ahead() {
+        end_ahead = 0;
+        len_ahead = 0;
+        if (n + 1 < a.N) {
+            end_ahead = cu_of(a.cu, a.cu64, n + 2);
+            len_ahead = a.kv_lens[n + 1];
+        }
+    }
 
     __device__ void enter() { items = (q.fresh + tokens - 1) / tokens; }
     __device__ Walk(const AttnParams &a_, int tokens_, const Share &s) : a(a_), tokens(tokens_) {
         left = s.left;
         first = true;
         h = m = off = items = n = 0;
-        q = ahead = {0, 0, 0};
+        q = {0, 0, 0};
         if (left <= 0) return;
         n = s.n;
-        q = seq_at(a, n, nullptr);
-        ahead = seq_at(a, n + 1, nullptr);
+        q = s.q;
+        read_ahead();
         enter();
         h = static_cast<int>(div_by(s.in_seq, s.cost));
         long long at = s.in_seq - h * s.cost;
@@ -352,10 +373,13 @@ struct Walk {
             m = 0;
             if (++h == a.HKV) {
                 h = 0;
+                // (the lengths have been checked)
                 do {
                     ++n;
-                    q = ahead;
-                    ahead = seq_at(a, n + 1, nullptr);
+                    q.t0 += q.fresh;
+                    q.fresh = n < a.N ? static_cast<int>(end_ahead) - q.t0 : 0;
+                    q.len = len_ahead;
+                    read_ahead();
                 } while (q.fresh == 0 && n < a.N);
                 enter();
             }
@@ -517,27 +541,31 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
         return;
     }
 
-    if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+    if (wp == 0) {
+        if (lane < C::kStages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
         }
-        for (int i = 0; i < kSegRing; ++i) {
-            mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 11);  // the warps but the one that hands them out
+        if (lane < kSegRing) {
+            mbar_init(&sh.seg_full[lane], 1);
+            mbar_init(&sh.seg_empty[lane], 11);  // the warps but the one that hands them out
         }
-        mbar_init(&sh.tail, 1);
-        mbar_init(&sh.drain, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.q_full[i], 1);
-            mbar_init(&sh.q_free[i], 1);
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_half[i], 4);
-            mbar_init(&sh.p_full[i], 4);
-            mbar_init(&sh.o_full[i], 1);
+        if (lane < 2) {
+            mbar_init(&sh.q_full[lane], 1);
+            mbar_init(&sh.q_free[lane], 1);
+            mbar_init(&sh.s_full[lane], 1);
+            mbar_init(&sh.p_half[lane], 4);
+            mbar_init(&sh.p_full[lane], 4);
+            mbar_init(&sh.o_full[lane], 1);
         }
-        mbar_init(&sh.ml_full, 4);
-        mbar_init(&sh.o_free, 4);
+        if (lane == 0) {
+            mbar_init(&sh.tail, 1);
+            mbar_init(&sh.drain, 1);
+            mbar_init(&sh.ml_full, 4);
+            mbar_init(&sh.o_free, 4);
+            sh.share.flags = 0;
+            sh.share.left = 0;
+        }
         fence_mbar_init();
     }
     if (wp == kMmaWarp) tmem_alloc(&sh.tmem, 512);
@@ -547,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
         if (p.q_map) prefetch_map(&p.tq);
     }
     pdl_trigger();
+    __syncthreads();
     find_share(a, 2 * p.tt, sh.share);
     __syncthreads();
     tc_fence_after();
@@ -599,13 +628,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             return e;
         };
         int2 now = fetch(g.lo), next = fetch(g.lo + batch);
-        ahead();
+        if (ld.base > 0) ahead();
         for (int i = 0, in = 0; i < tiles && ld.ok; ++i) {
+            if (i == 1 && ld.base == 0) ahead();
             const uint32_t load = ld.base + at(i);
             const int st = static_cast<int>(load % C::kStages);
             const int left = min(kTile, g.end - (g.lo + i) * kTile);  // rows that count
             const int grans = (left + gran - 1) / gran;
-            ld.ok = warp_wait(&empty[st], ((load / C::kStages) & 1) ^ 1);
+            ld.ok = ld.ok && warp_wait(&empty[st], ((load / C::kStages) & 1) ^ 1);
             if (!ld.ok) return;
             const bool patch = is_v && left < kTile;
             uint64_t *bar = patch ? &sh.tail : &full[st];
@@ -640,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                 next = fetch(g.lo + i + 1 + batch);
             }
         }
+        if (tiles == 1 && ld.base == 0) ahead();
         ld.base += 2 * tiles;
     };
     // a loader that gave up lets its copies in flight land before the block ends
@@ -696,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             const Segment cur = g;
             const bool two = cur.ntok > p.tt;
             // (the next one is handed out before this one's copies, so that its
-            // queries can be loaded early)
+            // queries can be loaded early; after the first copy at the very start)
             load_tiles(ld, cur, false, [&](int i) { return key_at(i, two); }, hand_out);
         }
         if (lane == 0) p.joint[blockIdx.x] = joint;
@@ -1055,8 +1086,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     // store then touches 8 lines instead of the 32 of a thread per
                     // row, which took 4 k cycles an item.
                     const int q = lane & 3;
+                    const uint32_t rows_in = __ballot_sync(0xffffffffu, tok >= 0);
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
+                        if (!(rows_in >> (16 * half) & 0xffffu)) continue;
                         float g0[2], g1[2];
                         bf16 *o[2];
                         float *po[2];
@@ -1154,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
 // Rows of the items that were cut: a warp per row,
 //   M = max_i m_i,  L = sum_i 2^(m_i - M) l_i,  o = sum_i 2^(m_i - M) o_i / L.
 // The first block also gathers the CTAs' flags into the status words.
-constexpr int kJoinRows = 32;  // rows of a block: 8 warps, 4 rows each
+constexpr int kJoinRows = 16;  // rows of a block: 8 warps, 4 rows each
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) gdn2_attn_combine_kernel(const __grid_constant__ KernelParams p) {
