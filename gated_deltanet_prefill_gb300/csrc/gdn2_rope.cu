@@ -13,9 +13,13 @@
 // squares, those that fetch the partner's 8 channels (half layout; in the
 // interleaved one the partner is in the lane) and 16 multiply-adds.
 //
-// Bound by memory: the bytes in and out are all there is.  A warp takes all
-// heads of a token when there are tokens enough to fill the GPU, and a slice
-// of them otherwise, so that a decode step is one row group per warp.
+// Bound by memory: 32768 tokens of 32 + 32 heads (half of each head rotated) take
+// 179 us, 6.00 TB/s of the 6.78 that a copy reaches; the append of 34997 tokens of
+// 32 + 32 + 32 heads to pages of 16 takes 266 us, 6.46 TB/s.  The packed fp32
+// instructions keep the issue slots below what the loads need.  A warp takes all
+// heads of a token when there are tokens enough to fill the GPU, and a slice of
+// them otherwise, so that a decode step is one row group per warp (128 tokens of
+// 40 heads: 4 us, of which the launch is most).
 #include "gdn2_attn_internal.cuh"
 #include "gdn2_tc.cuh"
 
@@ -26,6 +30,12 @@ using namespace tc;
 
 constexpr int kWarps = 4;    // warps per block
 constexpr int kUnroll = 4;   // row groups in flight per warp
+// Blocks per SM that the registers are cut for (72 a thread; a few of the
+// coefficients spill).  Measured on 32768 tokens of 64 heads and on the append of
+// 34997 tokens of 96: 200 and 288 us uncut (92 registers, 5 blocks), 187 and 269
+// with 6, 179 and 266 with 7, 179 and 268 with 8; 2 groups in flight at 8 blocks
+// 192 and 290, 8 groups at 4 blocks 205 and 284.
+constexpr int kMinBlocks = 7;
 // Resident warps that the slicing aims at, per SM.
 constexpr int kWarpsPerSm = 32;
 
@@ -144,16 +154,41 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
     else
         unpack8_bf(u, f);
 }
+// Pairs of fp32 values in 64-bit registers, and the packed operations on them (one
+// instruction for two).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 template <bool F16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    if (!F16) return pack8_bf(f);
-    return make_uint4(pack_f16_rn(f[0], f[1]), pack_f16_rn(f[2], f[3]), pack_f16_rn(f[4], f[5]),
-                      pack_f16_rn(f[6], f[7]));
+__device__ __forceinline__ void unpack8_pairs(const uint4 &u, uint64_t (&f)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = F16 ? unpack_h2(w[i]) : unpack_bf2(w[i]);
+        f[i] = pair(x.x, x.y);
+    }
 }
 
 // PAGED: keys and values go to their pages, and block 0 checks the tables.
 template <int D, bool F16, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(32 * kWarps) gdn2_rope_kernel(const __grid_constant__ RopeParams p, int slices,
+__global__ void __launch_bounds__(32 * kWarps, kMinBlocks) gdn2_rope_kernel(const __grid_constant__ RopeParams p, int slices,
                                                                 int rows_per_slice) {
     constexpr int L = D / 8;    // lanes per row
     constexpr int R = 32 / L;   // rows per warp and load
@@ -197,7 +232,7 @@ __global__ void __launch_bounds__(32 * kWarps) gdn2_rope_kernel(const __grid_con
     // rows [lo, hi) of one kind: queries or keys
     auto rows = [&](int lo, int hi, const bf16 *x, int64_t sx, bf16 *y, int64_t sy, const bf16 *w) {
         if (lo >= hi) return;
-        float A[8], B[8];
+        uint64_t A[4], B[4];  // of channels 2 e and 2 e + 1
         {
             float wa[8], wb[8];
 #pragma unroll
@@ -207,9 +242,9 @@ __global__ void __launch_bounds__(32 * kWarps) gdn2_rope_kernel(const __grid_con
                 unpack8<F16>(*reinterpret_cast<const uint4 *>(w + 8 * partner), wb);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                A[e] = wa[e] * cs[INTER ? e / 2 : e];
-                B[e] = INTER ? wb[e ^ 1] * (e & 1 ? sn[e / 2] : -sn[e / 2]) : wb[e] * sn[e];
+            for (int e = 0; e < 4; ++e) {
+                A[e] = INTER ? pair(wa[2 * e] * cs[e], wa[2 * e + 1] * cs[e]) : pair(wa[2 * e] * cs[INTER ? 0 : 2 * e], wa[2 * e + 1] * cs[INTER ? 0 : 2 * e + 1]);
+                B[e] = INTER ? pair(wb[2 * e + 1] * -sn[e], wb[2 * e] * sn[e]) : pair(wb[2 * e] * sn[INTER ? 0 : 2 * e], wb[2 * e + 1] * sn[INTER ? 0 : 2 * e + 1]);
             }
         }
         const int src = lane - c + partner;
@@ -224,33 +259,45 @@ __global__ void __launch_bounds__(32 * kWarps) gdn2_rope_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 if (h0 + i * R >= hi) break;  // the same for all lanes
-                float v[8], o[8];
-                unpack8<F16>(u[i], v);
+                uint64_t v[4], z[4];
+                unpack8_pairs<F16>(u[i], v);
                 float r = 1.f;
                 if (p.norm) {
-                    float sum = 0.f;
+                    uint64_t s2 = mul2(v[0], v[0]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+                    for (int e = 1; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
+                    const float2 t2 = unpair(s2);
+                    float sum = t2.x + t2.y;
 #pragma unroll
                     for (int d = L / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                     r = rsqrtf(sum * (1.f / D) + p.eps);
                 }
+                // the partners' values; zero where nothing turns (0 x inf is NaN)
                 if (INTER) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = r * (v[e] * A[e] + (turned ? v[e ^ 1] * B[e] : 0.f));
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 t2 = unpair(v[e]);
+                        z[e] = turned ? pair(t2.y, t2.x) : 0;
+                    }
                 } else {
                     uint4 q;
                     q.x = __shfl_sync(0xffffffffu, u[i].x, src);
                     q.y = __shfl_sync(0xffffffffu, u[i].y, src);
                     q.z = __shfl_sync(0xffffffffu, u[i].z, src);
                     q.w = __shfl_sync(0xffffffffu, u[i].w, src);
-                    float z[8];
-                    unpack8<F16>(q, z);
+                    if (!turned) q = make_uint4(0, 0, 0, 0);
+                    unpack8_pairs<F16>(q, z);
+                }
+                const uint64_t r2 = pair(r, r);
+                uint4 out;
+                uint32_t *o = &out.x;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = r * (v[e] * A[e] + (turned ? z[e] * B[e] : 0.f));
+                for (int e = 0; e < 4; ++e) {
+                    const float2 t2 = unpair(mul2(r2, fma2(z[e], B[e], mul2(v[e], A[e]))));
+                    o[e] = F16 ? pack_f16_rn(t2.x, t2.y) : pack_bf2(t2.x, t2.y);
                 }
                 const int h = h0 + i * R + sub;
-                if (h < hi) *reinterpret_cast<uint4 *>(y + h * sy + 8 * c) = pack8<F16>(o);
+                if (h < hi) *reinterpret_cast<uint4 *>(y + h * sy + 8 * c) = out;
             }
         }
     };
