@@ -1054,32 +1054,40 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                 arrive(&sh.ml_full);
             }
             if (TWO || x == 0) {
-                ok = warp_wait(&sh.o_full[x], o_ph[x] & 1);
+                // where the row goes, while the last product runs
+                const bool whole = g.slot < 0;
+                const int head = g.h * a.G + my_head;
+                const int64_t tok_row = static_cast<int64_t>(g.tok0) + max(tok, 0);
+                const int64_t part = static_cast<int64_t>(max(g.slot, 0)) * 2 * kTile + tile * kTile + row;
+                const uint64_t dst = tok < 0 ? 0
+                                     : whole ? reinterpret_cast<uint64_t>(a.out + tok_row * a.so_t + head * a.so_h)
+                                             : reinterpret_cast<uint64_t>(p.part_o + part * D);
                 float f0 = 1.f, f1 = 0.f;
                 if (merged) {
-                    ok = ok && warp_wait(&sh.o_full[1], o_ph[1] & 1) && warp_wait(&sh.ml_full, merges & 1);
+                    ok = warp_wait(&sh.ml_full, merges & 1);
                     const float2 ml = sh.ml[row];
-                    const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top * sl2;
+                    const float peak = fmaxf(m, ml.x), base = peak == -INFINITY ? 0.f : peak * sl2;
                     f0 = ex2(fmaf(m, sl2, -base));
                     f1 = ex2(fmaf(ml.x, sl2, -base));
-                    m = top;
+                    m = peak;
                     l = f0 * l + f1 * ml.y;
                 }
+                if (tok >= 0) {
+                    const float base = m == -INFINITY ? -INFINITY : m * sl2;
+                    if (!whole)
+                        p.part_ml[part] = make_float2(base, l);
+                    else if (a.lse)
+                        a.lse[tok_row * a.HQ + head] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+                }
+                if (whole) {
+                    const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+                    f0 *= inv;
+                    f1 *= inv;
+                }
+                ok = ok && warp_wait(&sh.o_full[x], o_ph[x] & 1) && (!merged || warp_wait(&sh.o_full[1], o_ph[1] & 1));
                 if (!ok) return;
                 tc_fence_after();
                 if (!idle) {
-                    const bool whole = g.slot < 0;
-                    const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                    f0 *= inv;
-                    f1 *= inv;
-                    if (tok >= 0) {
-                        const int64_t at = static_cast<int64_t>(g.tok0) + tok;
-                        const float base = m == -INFINITY ? -INFINITY : m * sl2;
-                        if (!whole)
-                            p.part_ml[static_cast<int64_t>(g.slot) * 2 * kTile + tile * kTile + row] = make_float2(base, l);
-                        else if (a.lse)
-                            a.lse[at * a.HQ + g.h * a.G + my_head] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
-                    }
                     // The rows out: the outputs are read in the shape of 16 lanes, a
                     // quad of threads per row, and exchanged within the quad so that
                     // it stores 64 consecutive bytes of the row (16 per thread): a
@@ -1090,25 +1098,20 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         if (!(rows_in >> (16 * half) & 0xffffu)) continue;
-                        float g0[2], g1[2];
-                        bf16 *o[2];
-                        float *po[2];
-                        bool in[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int src = 16 * half + 8 * h + (lane >> 2);  // the thread that has the row
-                            g0[h] = __shfl_sync(0xffffffffu, f0, src);
-                            g1[h] = __shfl_sync(0xffffffffu, f1, src);
-                            const int t = __shfl_sync(0xffffffffu, tok, src), hd = __shfl_sync(0xffffffffu, my_head, src);
-                            in[h] = t >= 0;
-                            o[h] = a.out + (static_cast<int64_t>(g.tok0) + max(t, 0)) * a.so_t + static_cast<int64_t>(g.h * a.G + hd) * a.so_h;
-                            po[h] = p.part_o + (static_cast<int64_t>(max(g.slot, 0)) * 2 * kTile + tile * kTile + 32 * (wp & 3) + src) * D;
-                        }
                         const uint32_t at = lanes + (static_cast<uint32_t>(16 * half) << 16);
                         uint32_t all[D / 64][32];  // [c / 64][4 n + 2 h + e]: row h, column c + 8 n + 2 q + e
                         __syncwarp();
 #pragma unroll
                         for (int c = 0; c < D; c += 64) tmem_ld_rows(tO(x) + at + c, all[c / 64]);
+                        float g0[2], g1[2];
+                        uint64_t o[2];  // 0: no row
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int src = 16 * half + 8 * h + (lane >> 2);  // the thread that has the row
+                            g0[h] = __shfl_sync(0xffffffffu, f0, src);
+                            g1[h] = merged ? __shfl_sync(0xffffffffu, f1, src) : 0.f;
+                            o[h] = __shfl_sync(0xffffffffu, dst, src);
+                        }
                         tmem_ld_wait();
 #pragma unroll
                         for (int c = 0; c < D; c += 64) {
@@ -1136,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                                             w[k] = F16 ? pack_f16_rn(y0, y1) : pack_bf2(y0, y1);
                                         }
                                         quad_transpose(w, q);
-                                        if (in[h]) *reinterpret_cast<uint4 *>(o[h] + c + 8 * (n + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+                                        if (o[h]) reinterpret_cast<uint4 *>(o[h])[c / 8 + n + q] = make_uint4(w[0], w[1], w[2], w[3]);
                                     }
                             } else {
 #pragma unroll
@@ -1147,8 +1150,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                                         const bool odd = q & 1;
                                         const uint32_t a0 = u[4 * n + 2 * h], a1 = u[4 * n + 2 * h + 1], b0 = u[4 * n + 4 + 2 * h], b1 = u[4 * n + 5 + 2 * h];
                                         const uint32_t r0 = __shfl_xor_sync(0xffffffffu, odd ? a0 : b0, 1), r1 = __shfl_xor_sync(0xffffffffu, odd ? a1 : b1, 1);
-                                        if (in[h])
-                                            *reinterpret_cast<uint4 *>(po[h] + c + 8 * (n + (q & 1)) + 2 * (q & 2)) =
+                                        if (o[h])
+                                            reinterpret_cast<uint4 *>(o[h])[(c + 8 * n) / 4 + 2 * (q & 1) + (q >> 1)] =
                                                 odd ? make_uint4(r0, r1, b0, b1) : make_uint4(a0, a1, r0, r1);
                                     }
                             }
