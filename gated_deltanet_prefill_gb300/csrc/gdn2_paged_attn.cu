@@ -33,8 +33,10 @@
 // outputs of its own that are merged at the end of the segment.  Either way one
 // group's softmax runs while the tensor cores work for the other.
 //
-// The last tile's value rows past the range are zeroed in shared memory (the
-// cache may hold anything there, and 0 x NaN is NaN); the keys' scores are masked.
+// The value rows of an item's first and last tile that none of its rows attends to
+// (before the window, past the causal range) are zeroed in shared memory: the
+// cache may hold anything there, and 0 x NaN is NaN.  The keys' scores are masked.
+// Pages wholly before the window are not read, nor their table entries.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -52,6 +54,7 @@ constexpr int kTile = 128;      // rows of a tile, keys of a tile
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
 constexpr int kSegRing = 8;     // segments in flight between the warps
+constexpr int kMaxLen = 0x7fff0000;  // of a cached sequence: tiles are rounded up in 32 bits
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Registers: three warpgroups of 168 at launch, 64512 in all; the two softmax
@@ -64,9 +67,9 @@ constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 struct __align__(16) Segment {
     int tok0, h, ntok, slot;
     int lo, hi;
-    int end;    // keys from `end` on are not attended to
+    int begin, end;  // no row of the item attends to a key outside
     int place;  // of the first new token in its cached sequence
-    int seq, pad[3];
+    int seq, pad[2];
 };
 // The item whose pieces the combine kernel joins: the first in slot `slot`,
 // then `more` in slots 2 (cta + 1), 2 (cta + 2), ...
@@ -107,14 +110,14 @@ Layout layout_of(const gdn2_attn_dims &d) {
 
 // ------------------------------------------------------------- the shares
 struct Span {
-    int lo, hi, end;  // key tiles, first key past the range
+    int lo, hi, begin, end;  // key tiles, keys
 };
 // Key tiles of the new tokens j0 .. j1 of a sequence of `len` cached tokens.
 __device__ __forceinline__ Span key_span(const AttnParams &a, int len, int fresh, int j0, int j1) {
     Span s;
     s.end = a.causal ? max(0, len - fresh + j1) : len;
-    const int begin = a.window >= 0 ? max(0, len - fresh + j0 - a.window) : 0;
-    s.lo = begin / kTile;
+    s.begin = a.window >= 0 ? max(0, max(0, len - fresh + j0) - a.window) : 0;
+    s.lo = s.begin / kTile;
     s.hi = (s.end + kTile - 1) / kTile;
     if (s.hi < s.lo) s.hi = s.lo;
     return s;
@@ -178,7 +181,7 @@ __device__ __forceinline__ Seq seq_at(const AttnParams &a, int n, int *flags) {
     const int len = a.kv_lens[n];
     if (c0 > c1 || c0 < 0 || c1 > a.T) {
         if (flags) *flags |= kBadCu;
-    } else if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page_size) {
+    } else if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.max_pages) * a.page_size) {
         if (flags) *flags |= kBadPages;
     } else {
         q.t0 = static_cast<int>(c0);
@@ -362,6 +365,7 @@ struct Walk {
         g.slot = off > 0 || take < cost ? 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1) : -1;
         g.lo = s.lo + off;
         g.hi = s.hi == s.lo ? g.lo : g.lo + take;
+        g.begin = s.begin;
         g.end = s.end;
         g.place = q.len - q.fresh + j0;
         rest = cost - off - take;
@@ -617,7 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             t += lane / per;
             int2 e = make_int2(0, 0);
             const int64_t key = static_cast<int64_t>(t) * kTile + (lane % per) * gran;
-            if (t < g.hi && key < g.end) {
+            if (t < g.hi && key + gran <= g.begin) {
+                e.x = static_cast<int>(a.num_pages);  // before the window, where the page may be gone: zeros
+            } else if (t < g.hi && key < g.end) {
                 const int col = static_cast<int>(key) / a.page_size;
                 e = make_int2(row[col], static_cast<int>(key) - col * a.page_size);
                 if (e.x < 0 || e.x >= a.num_pages) {
@@ -627,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             }
             return e;
         };
+        int skip = max(0, g.begin - g.lo * kTile);          // first rows of the first tile that do not count
         int2 now = fetch(g.lo), next = fetch(g.lo + batch);
         if (ld.base > 0) ahead();
         for (int i = 0, in = 0; i < tiles && ld.ok; ++i) {
@@ -637,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             const int grans = (left + gran - 1) / gran;
             ld.ok = ld.ok && warp_wait(&empty[st], ((load / C::kStages) & 1) ^ 1);
             if (!ld.ok) return;
-            const bool patch = is_v && left < kTile;
+            const bool patch = is_v && (left < kTile || skip > 0);
             uint64_t *bar = patch ? &sh.tail : &full[st];
             uint8_t *dst = smem + C::kRing + st * C::kStageBytes;
             if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(grans * gran * 128 * NB));
@@ -651,18 +658,19 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                 tma_load_4d(dst + my_cb * (kTile * 128) + my_gr * gran * 128, is_v ? &p.tv : &p.tk, c, bar);
             }
             ld.used = load + 1;
-            if (patch) {  // zero the rows past the range, once the copies are in
+            if (patch) {  // zero the rows outside the range, once the copies are in
                 ld.ok = warp_wait(&sh.tail, ld.tail_ph);
                 if (!ld.ok) return;
                 ld.tail_ph ^= 1;
-                for (int k = lane; k < (kTile - left) * NB * 8; k += 32) {
-                    const int r = left + k / (NB * 8), q = k % (NB * 8);
+                for (int k = lane; k < (skip + kTile - left) * NB * 8; k += 32) {
+                    const int n = k / (NB * 8), r = n < skip ? n : left + n - skip, q = k % (NB * 8);
                     *reinterpret_cast<uint4 *>(dst + (q >> 3) * (kTile * 128) + r * 128 + (q & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[st]);
+                skip = 0;
             }
             if (++in == batch) {
                 in = 0;
@@ -937,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             // keys [from, upto) for this row; rows without a token take what they get
             const int place = g.place + (tok < 0 ? 0 : tok);
             const int upto = tok < 0 ? 0x7fffffff : a.causal ? place + 1 : g.end;
-            const int from = tok >= 0 && a.window >= 0 ? place - a.window : 0;
+            const int from = tok >= 0 && a.window >= 0 ? max(0, max(0, place) - a.window) : 0;
             const bool idle = !__any_sync(0xffffffffu, tok >= 0);  // no row of the warp has a token
             constexpr int stride = TWO ? 1 : 2;
             const int begin = TWO ? 0 : x;

@@ -492,3 +492,127 @@ def test_chunks_then_tokens_equal_one_pass(cuda_lib):
         bound = 2 * UNIT["torch.float16"] * 4 + 1e-3  # both roundings of values up to 4
         assert (part.float() - whole[rows].float()).abs().max() <= bound
         assert (pl - wl[rows]).abs().max() <= 4e-4
+
+
+def drop_before_window(c, window, value=float("nan")):
+    """What lies before the window of each sequence's first new token: slots overwritten, pages out of the table."""
+    for n, (new, total) in enumerate(zip(c.new, c.total)):
+        gone = max(0, total - new - window) if new else total
+        for j in range(gone):
+            page = c.table[n, j // c.page]
+            c.k[page, j % c.page], c.v[page, j % c.page] = value, value
+        c.table[n, :gone // c.page] = -1
+
+
+@pytest.mark.parametrize("new,past,page,HQ,HKV,D,window", [
+    ([1], [1000], 16, 4, 2, 128, 100),
+    ([1, 1, 1], [129, 640, 3000], 8, 2, 1, 64, 127),
+    ([30, 2], [900, 70], 64, 4, 1, 128, 0),
+    ([300], [700], 24, 8, 2, 64, 333),
+    ([5, 7], [513, 511], 256, 6, 2, 128, 200),
+])
+def test_attention_pages_before_the_window_may_be_gone(cuda_lib, new, past, page, HQ, HKV, D, window):
+    g = gen(31)
+    c = Cache(g, new, past, page, HKV, D, fill=float("nan"))
+    table = c.table.clone()
+    drop_before_window(c, window)
+    q = normal(g, sum(new), HQ, D)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    out, lse = attn.paged_attn_fwd(q, *c.args(), window_left=window, return_lse=True, workspace=ws)
+    assert attn.device_status(ws) == 0
+    c.table = table  # the reference's gather reads the slots that the mask then leaves out
+    check_attn(q, c, out, lse, window=window)
+
+
+def test_attention_widest_windows(cuda_lib):
+    """Windows up to the largest integer, rows without a key among them: as without a window."""
+    g = gen(32)
+    c = Cache(g, [40, 9, 300], [100, 0, 0], 16, 2, 64)
+    c.lens.copy_(ints([140, 4, 170]))
+    q = normal(g, 349, 4, 64)
+    want, wl = attn.paged_attn_fwd(q, *c.args(), return_lse=True)
+    check_attn(q, c, want, wl)
+    for window in (140, 2 ** 31 - 2, 2 ** 31 - 1):
+        out, lse = attn.paged_attn_fwd(q, *c.args(), return_lse=True, window_left=window)
+        check_attn(q, c, out, lse, window=window)
+
+
+LONG = [
+    # sequences past one round of the shares' sum, and items past one warp's
+    ([1] * 500 + [2] * 300 + [0] * 7, [(53 * i) % 260 for i in range(807)], 16, 2, 1, 64, True, -1),
+    ([3, 0, 1, 40] * 250, [(17 * i) % 90 for i in range(1000)], 8, 8, 2, 128, True, 31),
+    ([1300], [0], 64, 8, 1, 64, True, -1),
+    ([1100, 700, 5], [77, 1, 300], 32, 16, 1, 64, True, -1),
+    ([1500], [40], 16, 8, 1, 64, True, 150),
+    ([1111], [200], 16, 8, 1, 64, False, -1),
+    ([20, 600, 1], [128, 500, 90], 40, 32, 1, 128, True, -1),
+]
+
+
+@pytest.mark.parametrize("new,past,page,HQ,HKV,D,causal,window", LONG)
+def test_attention_many_sequences_and_items(cuda_lib, new, past, page, HQ, HKV, D, causal, window):
+    g = gen(len(new) + sum(new))
+    c = Cache(g, new, past, page, HKV, D, fill=float("nan"))
+    q = normal(g, sum(new), HQ, D)
+    out, lse = attn.paged_attn_fwd(q, *c.args(), causal=causal, window_left=window, return_lse=True)
+    check_attn(q, c, out, lse, causal, window)
+
+
+def test_attention_long_sequence_with_rows_without_keys(cuda_lib):
+    """More new tokens than cached ones in a sequence of many items."""
+    g = gen(33)
+    c = Cache(g, [1200, 3], [0, 50], 16, 1, 64)
+    c.lens.copy_(ints([700, 53]))
+    q = normal(g, 1203, 8, 64)
+    out, lse = attn.paged_attn_fwd(q, *c.args(), return_lse=True)
+    check_attn(q, c, out, lse)
+    assert (out[:500] == 0).all() and torch.isneginf(lse[:500]).all()
+
+
+def test_attention_broadcast_queries(cuda_lib):
+    """Queries expanded over heads or tokens (zero strides) equal their copies."""
+    g = gen(34)
+    c = Cache(g, [7, 150, 1], [20, 0, 400], 16, 2, 128)
+    for q in (normal(g, 158, 1, 128).expand(158, 6, 128), normal(g, 1, 6, 128).expand(158, 6, 128)):
+        out, lse = attn.paged_attn_fwd(q, *c.args(), return_lse=True)
+        want, wl = attn.paged_attn_fwd(q.contiguous(), *c.args(), return_lse=True)
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        check_attn(q, c, out, lse)
+
+
+def test_nothing_is_written_past_the_buffers(cuda_lib):
+    """Outputs and workspaces of exactly the stated size between canaries; a used workspace changes no result."""
+    g = gen(35)
+    guard = 4096
+
+    def fenced(n):
+        buf = torch.full((n + 2 * guard,), 0x5A, dtype=torch.uint8, device="cuda")
+        return buf, buf[guard:guard + n]
+
+    buffers = []
+    for new, past, HQ, HKV, D in (([1] * 5, [0, 9, 500, 900, 17], 8, 2, 128), ([200, 3], [0, 700], 4, 4, 64),
+                                  ([1], [4000], 2, 1, 64)):
+        c = Cache(g, new, past, 16, HKV, D)
+        T = sum(new)
+        q, k, v = normal(g, T, HQ, D), normal(g, T, HKV, D), normal(g, T, HKV, D)
+        f, _ = attn.rope_frequencies(D)
+        size = T * HQ * D * 2
+        qo, out, lse, aws = fenced(size), fenced(size), fenced(T * HQ * 4), fenced(64)
+        dims = attn.AttnDims()
+        assert attn.load().gdn2_attn_dims_init(dims, T, len(new), HQ, HKV, D, c.k.shape[0], 16, c.table.shape[1]) == 0
+        ws = fenced(attn.load().gdn2_paged_attn_workspace_bytes(dims))
+        view = lambda b: b[1].view(BF).view(T, HQ, D)  # noqa: E731
+        attn.append_kv(k, v, *c.args(), q=q, inv_freq=f, q_out=view(qo), workspace=aws[1])
+        first = None
+        for fill in (0, 255, None):
+            if fill is not None:
+                ws[1].fill_(fill)
+            out[1].fill_(0x33)
+            attn.paged_attn_fwd(view(qo), *c.args(), out=view(out), lse=lse[1].view(torch.float32), workspace=ws[1])
+            assert attn.device_status(ws[1]) == 0 and attn.device_status(aws[1]) == 0
+            first = view(out).clone() if first is None else first
+            assert torch.equal(first, view(out))
+        check_attn(view(qo), c, view(out), lse[1].view(torch.float32).view(T, HQ))
+        buffers += [qo[0], out[0], lse[0], aws[0], ws[0]]
+    for b in buffers:
+        assert (b[:guard] == 0x5A).all() and (b[-guard:] == 0x5A).all()
