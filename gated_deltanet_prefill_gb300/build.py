@@ -40,7 +40,8 @@ def _stale(lib=LIB) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = sources() + [f for d, x in ((CSRC, "*.cuh"), (CSRC, "*.h"), (INCLUDE, "*.h"))
+                        for f in glob.glob(os.path.join(d, x))]
     return any(os.path.getmtime(f) > t for f in deps)
 
 

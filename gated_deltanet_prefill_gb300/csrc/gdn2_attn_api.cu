@@ -4,7 +4,7 @@
 #include <stdint.h>
 #include <string.h>
 
-#include "gdn2_attn_internal.cuh"
+#include "gdn2_attn_internal.h"
 
 namespace gdn2 {
 namespace {

@@ -1,4 +1,6 @@
 // Internal declarations of the attention-layer operators (include/gdn2_attn.h).
+// Only their own sources include it, so it is no part of the GDN-2 kernels' shared
+// headers (*.cuh), by which their profiles are matched.
 #pragma once
 
 #include "gdn2_attn.h"

@@ -41,7 +41,7 @@
 
 #include <type_traits>
 
-#include "gdn2_attn_internal.cuh"
+#include "gdn2_attn_internal.h"
 #include "gdn2_tc.cuh"
 
 namespace gdn2 {
@@ -54,7 +54,6 @@ constexpr int kTile = 128;      // rows of a tile, keys of a tile
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
 constexpr int kSegRing = 8;     // segments in flight between the warps
-constexpr int kMaxLen = 0x7fff0000;  // of a cached sequence: tiles are rounded up in 32 bits
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Registers: three warpgroups of 168 at launch, 64512 in all; the two softmax
@@ -181,7 +180,7 @@ __device__ __forceinline__ Seq seq_at(const AttnParams &a, int n, int *flags) {
     const int len = a.kv_lens[n];
     if (c0 > c1 || c0 < 0 || c1 > a.T) {
         if (flags) *flags |= kBadCu;
-    } else if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.max_pages) * a.page_size) {
+    } else if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page_size) {
         if (flags) *flags |= kBadPages;
     } else {
         q.t0 = static_cast<int>(c0);

@@ -20,7 +20,7 @@
 // heads of a token when there are tokens enough to fill the GPU, and a slice of
 // them otherwise, so that a decode step is one row group per warp (128 tokens of
 // 40 heads: 4 us, of which the launch is most).
-#include "gdn2_attn_internal.cuh"
+#include "gdn2_attn_internal.h"
 #include "gdn2_tc.cuh"
 
 namespace gdn2 {

@@ -50,8 +50,8 @@ extern "C" {
  *
  * Supported: D in {64, 128}; rot_dim a multiple of 16 in 0 .. D; page_size a
  * multiple of 8; num_pages >= 1; HQ a multiple of HKV with at most 128 query
- * heads per key head (gdn2_qk_norm_rope takes any two head counts);
- * T_tot < 2^31 - 2^16.
+ * heads per key head (gdn2_qk_norm_rope takes any two head counts); T_tot and
+ * max_pages * page_size below 2^31 - 2^16.
  */
 typedef struct gdn2_attn_dims {
     int64_t T_tot;
@@ -164,8 +164,8 @@ GDN2_API size_t gdn2_paged_attn_workspace_bytes(const gdn2_attn_dims *dims);
  * infinities included, and pages wholly before that window may be gone: their
  * table entries are not read.  A NaN or an infinity among the values that one
  * new token attends to may reach other new tokens of its sequence whose mask
- * leaves it out (as 0 x NaN).  A kv_len below 0, past 2^31 - 2^16 or past max_pages
- * * page_size is reported as GDN2_ERR_PAGES and a bad cu_seqlens as
+ * leaves it out (as 0 x NaN).  A kv_len below 0 or past max_pages * page_size is
+ * reported as GDN2_ERR_PAGES and a bad cu_seqlens as
  * GDN2_ERR_CU_SEQLENS (gdn2_device_status on the workspace); the call then
  * writes nothing.  A table entry in reach that is not in 0 .. num_pages - 1 is
  * reported as GDN2_ERR_PAGES; the outputs of its sequence are then undefined.
