@@ -7,9 +7,9 @@
 // read.  An item is (sequence, key head, up to two row tiles) with its range of
 // 128-key tiles (after the causal and window masks).
 //
-// Work.  The items' key tiles, laid end to end, are cut into equal shares, one
-// per CTA (one CTA per SM), wherever the cuts fall: a share is a run of segments
-// (item, key tiles).  An item cut into several segments leaves unnormalised sums
+// Work.  The items' key tiles, laid end to end (with an allowance per item), are
+// cut into equal shares, one per CTA (one CTA per SM), wherever the cuts fall: a
+// share is a run of segments (item, key tiles).  An item cut into several segments leaves unnormalised sums
 // and their maxima in the workspace, and the combine kernel joins them in the
 // order of the segments.  So one long sequence, many short ones and any mixture
 // fill the GPU alike, and the result does not depend on timing.  Every CTA finds
@@ -53,6 +53,12 @@ constexpr int kMaxCtas = 152;   // shares at most (SMs of a GB300)
 constexpr int kTile = 128;      // rows of a tile, keys of a tile
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
+// What an item of two row tiles costs beside its key tiles, in key tiles: its
+// queries, its first softmax and its epilogue, when the tensor cores wait.
+// Measured on 8 chunks of 396 .. 3235 tokens (16 heads; 4 to 13 items per CTA): 286 us
+// without, 276 with 1, 267 with 2 and 3, 270 with 4, 276 with 6; 16384 tokens of
+// one sequence 734 -> 717.  An item of one row tile hides it behind its loads.
+constexpr int kLead = 2;
 constexpr int kSegRing = 8;     // segments in flight between the warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -121,10 +127,16 @@ __device__ __forceinline__ Span key_span(const AttnParams &a, int len, int fresh
     if (s.hi < s.lo) s.hi = s.lo;
     return s;
 }
-// What an item costs: its key tiles, at least 1 (an item without keys writes zeros).
+// What an item costs beside its key tiles (the items have `tokens` new tokens but for
+// the last of a sequence; more than half of that makes two row tiles).
+__device__ __forceinline__ int lead_of(int fresh, int tokens, int m) {
+    return min(fresh - m * tokens, tokens) > tokens / 2 ? kLead : 0;
+}
+// What an item costs: its key tiles, at least 1 (an item without keys writes zeros),
+// after the lead.
 __device__ __forceinline__ int item_cost(const AttnParams &a, int len, int fresh, int tokens, int m) {
     const Span s = key_span(a, len, fresh, m * tokens, min(fresh, (m + 1) * tokens));
-    return max(1, s.hi - s.lo);
+    return max(1, s.hi - s.lo) + lead_of(fresh, tokens, m);
 }
 
 // sum over i < n of floor((a i + b) / 128); a n + b < 2^32.
@@ -159,10 +171,11 @@ __device__ __forceinline__ bool closed_form(const AttnParams &a, int len, int fr
 // The cost of a sequence's first `items` items.
 __device__ long long cost_of(const AttnParams &a, int len, int fresh, int tokens, int items) {
     if (items <= 0) return 0;
-    if (!a.causal) return static_cast<long long>(items) * max(1, (len + kTile - 1) / kTile);
+    const long long lead = static_cast<long long>(items - 1) * kLead + lead_of(fresh, tokens, items - 1);
+    if (!a.causal) return lead + static_cast<long long>(items) * max(1, (len + kTile - 1) / kTile);
     // item m: ceil((len - fresh + min(fresh, (m + 1) tokens)) / 128); the last one apart
     const long long last = (len - fresh + min(static_cast<long long>(fresh), static_cast<long long>(items) * tokens) + kTile - 1) / kTile;
-    return last + floor_sum(items - 1, tokens, static_cast<uint32_t>(len - fresh) + tokens + kTile - 1);
+    return lead + last + floor_sum(items - 1, tokens, static_cast<uint32_t>(len - fresh) + tokens + kTile - 1);
 }
 
 __device__ __forceinline__ long long div_by(long long x, long long y) {
@@ -285,7 +298,7 @@ __device__ void find_share(const AttnParams &a, int tokens, Share &s) {
 struct Walk {
     const AttnParams &a;
     int tokens;
-    int n, h, m, off;       // item, key tiles of it already given out
+    int n, h, m, off;       // item, how much of its cost has been given out
     int items;              // row-tile groups of the sequence
     long long left;
     bool first;
@@ -355,21 +368,23 @@ struct Walk {
         if (left <= 0) return false;
         const int j0 = m * tokens;
         const Span s = key_span(a, q.len, q.fresh, j0, min(q.fresh, j0 + tokens));
-        const int cost = max(1, s.hi - s.lo);
+        const int lead = lead_of(q.fresh, tokens, m), tiles = max(1, s.hi - s.lo), cost = lead + tiles;
         const int take = static_cast<int>(min(static_cast<long long>(cost - off), left));
+        const int from = max(0, off - lead), to = max(0, off + take - lead);  // key tiles
+        left -= take;
+        if (to == from) return false;  // the share ends in the item's lead: the next one has it all
         g.seq = n;
         g.tok0 = q.t0 + j0;
         g.h = h;
         g.ntok = min(tokens, q.fresh - j0);
-        g.slot = off > 0 || take < cost ? 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1) : -1;
-        g.lo = s.lo + off;
-        g.hi = s.hi == s.lo ? g.lo : g.lo + take;
+        g.slot = from > 0 || to < tiles ? 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1) : -1;
+        g.lo = s.lo + from;
+        g.hi = s.hi == s.lo ? g.lo : s.lo + to;
         g.begin = s.begin;
         g.end = s.end;
         g.place = q.len - q.fresh + j0;
         rest = cost - off - take;
-        if (off > 0) rest = -rest;  // only the piece that begins the item reports the cut
-        left -= take;
+        if (from > 0) rest = -rest;  // only the piece that begins the item reports the cut
         first = false;
         off = 0;
         if (++m == items) {
