@@ -535,6 +535,11 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
     return r;
 }
 
+// The lowest n bits set (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0 : (1u << n) - 1;
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -980,12 +985,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     tmem_ld_wait();
                     if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
 #pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c >= hi) u[c >> 5][c & 31] = 0xff800000u;
-                        if (a.window >= 0) {
+                        for (int c = 0; c < 4; ++c) {
+                            // bit e: key 32 c + e is one of the row's
+                            const uint32_t bits = low_bits(hi - 32 * c) & ~low_bits(lo - 32 * c);
 #pragma unroll
-                            for (int c = 0; c < 128; ++c)
-                                if (c < lo) u[c >> 5][c & 31] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (!(bits >> e & 1)) u[c][e] = 0xff800000u;
                         }
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1121,10 +1126,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     for (int half = 0; half < 2; ++half) {
                         if (!(rows_in >> (16 * half) & 0xffffu)) continue;
                         const uint32_t at = lanes + (static_cast<uint32_t>(16 * half) << 16);
-                        uint32_t all[D / 64][32];  // [c / 64][4 n + 2 h + e]: row h, column c + 8 n + 2 q + e
+                        uint32_t u[32];  // [4 n + 2 h + e]: row h, column c + 8 n + 2 q + e
                         __syncwarp();
-#pragma unroll
-                        for (int c = 0; c < D; c += 64) tmem_ld_rows(tO(x) + at + c, all[c / 64]);
+                        tmem_ld_rows(tO(x) + at, u);
                         float g0[2], g1[2];
                         uint64_t o[2];  // 0: no row
 #pragma unroll
@@ -1134,10 +1138,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                             g1[h] = merged ? __shfl_sync(0xffffffffu, f1, src) : 0.f;
                             o[h] = __shfl_sync(0xffffffffu, dst, src);
                         }
-                        tmem_ld_wait();
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 64) {
-                            uint32_t(&u)[32] = all[c / 64];
+                            if (c > 0) tmem_ld_rows(tO(x) + at + c, u);
+                            tmem_ld_wait();
                             if (merged) {
                                 uint32_t v[32];
                                 tmem_ld_rows(tO(1) + at + c, v);
