@@ -414,6 +414,7 @@ struct Small {
     uint64_t seg_full[kSegRing], seg_empty[kSegRing];
     uint64_t q_full[2], q_free[2];                     // of row tile t
     uint64_t s_full[2], p_half[2], p_full[2], o_full[2];  // of stream x
+    uint64_t s_free[2], p_free[2];  // and with weights apart: scores read, weights used
     uint64_t ml_full, o_free;  // one row tile: group 1's statistics are in; group 0 has read the outputs
     Segment seg[kSegRing];
     Share share;
@@ -427,6 +428,10 @@ struct Cfg {
     static constexpr int kQBytes = kTile * D * 2;
     static constexpr int kStages = D == 128 ? 5 : 10;  // what fits beside the query tiles
     static constexpr int kRing = 2 * kQBytes;
+    // Weights apart: they have Tensor Memory of their own, so that the next scores
+    // are computed while the softmax works on these (it holds them in registers).
+    // With D = 128 scores and outputs take it all and the weights replace the scores.
+    static constexpr bool kApart = D == 64;
     static constexpr int kShared = kRing + kStages * kStageBytes;  // the barriers and small arrays
     static constexpr int kSmem = kShared + static_cast<int>(sizeof(Small<kStages>));
     static_assert(kSmem <= 232448, "shared memory of a block");
@@ -580,6 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             mbar_init(&sh.p_half[lane], 4);
             mbar_init(&sh.p_full[lane], 4);
             mbar_init(&sh.o_full[lane], 1);
+            mbar_init(&sh.s_free[lane], 4);
+            mbar_init(&sh.p_free[lane], 1);
         }
         if (lane == 0) {
             mbar_init(&sh.tail, 1);
@@ -604,9 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
     tc_fence_after();
     const uint32_t tm = sh.tmem;
     const uint32_t sQ = smem_u32(smem), sRing = smem_u32(smem + C::kRing);
-    // Tensor Memory columns: scores of stream x at 128 x, its outputs after them
+    // Tensor Memory columns: scores of stream x at 128 x, the outputs after them, the
+    // weights (16 bits, 64 columns) after those or in the scores' place
     auto tS = [&](int x) { return tm + 128 * x; };
-    auto tO = [&](int x) { return tm + 256 + 128 * x; };
+    auto tO = [&](int x) { return tm + 256 + D * x; };
+    auto tP = [&](int x) { return C::kApart ? tm + 256 + 2 * D + 64 * x : tS(x); };
     auto fail = [&]() { atomicOr(&sh.share.flags, kTimeout); };
     auto few_regs = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); };
     // the i-th segment of the share; its last reader in a warp releases it
@@ -618,11 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
 
     // Keys or values of a segment's tiles into the ring, by one warp.  `at`: the
     // place of tile i's load among the segment's 2 x tiles, in the order in which
-    // the products take them: K0 V0 K1 V1 .. with two row tiles, with one the keys
-    // run two tiles ahead of the values.  The releases come in the same order, so
-    // that a stage's emptiness is never mistaken for an earlier one's.
-    auto key_at = [](int i, bool two) { return two ? 2 * i : i < 2 ? i : 2 * i - 1; };
-    auto value_at = [](int i, int tiles, bool two) { return two ? 2 * i + 1 : i <= tiles - 2 ? 2 + 2 * i : 2 * tiles - 1; };
+    // the products take them: first n keys' tiles, then values and keys in turn.  The
+    // releases come in the same order, so that a stage's emptiness is never
+    // mistaken for an earlier one's.
+    auto keys_ahead = [](bool two) { return (two ? 1 : 2) + (C::kApart ? 1 : 0); };
+    auto key_at = [&](int i, bool two) { return i < keys_ahead(two) ? i : 2 * i - keys_ahead(two) + 1; };
+    auto value_at = [&](int i, int tiles, bool two) { return min(2 * i + keys_ahead(two), tiles + i); };
     struct Loader {
         uint32_t base = 0, used = 0;  // loads of the segments before; one past this warp's last
         int tail_ph = 0;
@@ -838,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             constexpr uint32_t kIdO = idesc_f16kind(kTile, D, false, true, !F16);
             uint32_t taken = 0;                  // stages taken so far
             uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+            uint32_t s_ph[2] = {1, 1};           // of s_free; the first wait passes
             bool ok = true;
             const uint32_t dq = desc_lo(sQ, 16);
             auto stage = [&](uint32_t i) { return sRing + (i % C::kStages) * C::kStageBytes; };
@@ -845,6 +856,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             // S of stream x = Q K^T with row tile t; then the stage is free if `last`, and
         // the queries' tile if `q_last`
             auto scores = [&](int x, int t, uint32_t k, bool last, bool q_last) {
+                if (C::kApart) {
+                    ok = ok && mbar_wait(&sh.s_free[x], s_ph[x]);
+                    s_ph[x] ^= 1;
+                }
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t dk = desc_lo(stage(k), 16);
@@ -867,14 +882,15 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
-                    mma_ts(tO(x), tS(x) + 8 * kk, dv + 128 * kk, kIdO, kk > 0 || !first);
+                    mma_ts(tO(x), tP(x) + 8 * kk, dv + 128 * kk, kIdO, kk > 0 || !first);
                 ok = mbar_wait(&sh.p_full[x], p_ph[x]);
                 p_ph[x] ^= 1;
                 if (!ok) return;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = kTile / 32; kk < kTile / 16; ++kk)
-                    mma_ts(tO(x), tS(x) + 8 * kk, dv + 128 * kk, kIdO, 1);
+                    mma_ts(tO(x), tP(x) + 8 * kk, dv + 128 * kk, kIdO, 1);
+                if (C::kApart) mma_commit(&sh.p_free[x]);
                 if (free) mma_commit(&empty[v % C::kStages]);
                 if (done) mma_commit(&sh.o_full[x]);
             };
@@ -898,8 +914,21 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     wait_q(1);
                     scores(1, 1, k, true, tiles == 1);
                     for (int i = 0; i < tiles && ok; ++i) {
-                        const uint32_t v = taken++;
                         const bool more = i + 1 < tiles;
+                        if (C::kApart) {
+                            if (more) {
+                                k = taken++;
+                                wait_stage(k);
+                                scores(0, 0, k, false, i + 2 == tiles);
+                                scores(1, 1, k, true, i + 2 == tiles);
+                            }
+                            const uint32_t v = taken++;
+                            wait_stage(v);
+                            output(0, v, i == 0, false, !more);
+                            output(1, v, i == 0, true, !more);
+                            continue;
+                        }
+                        const uint32_t v = taken++;
                         if (more) k = taken++;
                         wait_stage(v);
                         output(0, v, i == 0, false, !more);
@@ -917,14 +946,17 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                         scores(1, 0, k, true, tiles == 2);
                     }
                     for (int i = 0; i < tiles && ok; ++i) {
-                        const uint32_t v = taken++;
-                        wait_stage(v);
-                        output(i & 1, v, i < 2, true, i + 2 >= tiles);
-                        if (i + 2 < tiles) {
+                        auto next = [&] {
+                            if (i + 2 >= tiles) return;
                             k = taken++;
                             wait_stage(k);
                             scores(i & 1, 0, k, true, i + 3 == tiles);
-                        }
+                        };
+                        if (C::kApart) next();
+                        const uint32_t v = taken++;
+                        wait_stage(v);
+                        output(i & 1, v, i < 2, true, i + 2 >= tiles);
+                        if (!C::kApart) next();
                     }
                 }
             }
@@ -977,12 +1009,24 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                 // group 1's outputs of the last merged segment have to be read
                 if (x == 1 && i == begin && merges > 0) ok = ok && warp_wait(&sh.o_free, (merges - 1) & 1);
                 if (!ok) break;
+                // Waits until the stream's last product is in and weights and outputs may
+                // be written.  (With the weights in the scores' place it is: these
+                // scores followed it.)
+                auto used = [&] {
+                    if (!C::kApart || steps == 0) return;
+                    ok = warp_wait(&sh.p_free[x], (steps - 1) & 1);
+                    tc_fence_after();
+                };
                 if (!idle) {
                     tc_fence_after();
                     uint32_t u[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(tS(x) + lanes + 32 * c, u[c]);
                     tmem_ld_wait();
+                    if (C::kApart) {
+                        tc_fence_before();
+                        arrive(&sh.s_free[x]);
+                    }
                     if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -1009,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                             const float f = grow ? ex2((m - top) * sl2) : 1.f;
                             if (grow) m = top;
                             l *= f;
-                            // the stream's last product is in: these scores followed it
+                            used();
 #pragma unroll 1
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t o[32];
@@ -1059,7 +1103,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                             }
                             if (n > 0) finish(n - 1, e);
                         }
-                        if (n > 0 && n % 4 == 0) tmem_st16(tS(x) + lanes + 4 * (n - 4), w);
+                        if (n == 4) used();
+                        if (n > 0 && n % 4 == 0) tmem_st16(tP(x) + lanes + 4 * (n - 4), w);
                         if (n == 9) {  // the first half of the keys: their product may begin
                             tmem_st_wait();
                             tc_fence_before();
@@ -1071,6 +1116,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     tmem_st_wait();
                     tc_fence_before();
                 } else {
+                    if (C::kApart) arrive(&sh.s_free[x]);
+                    used();  // each phase is awaited, so that none is taken for another
                     arrive(&sh.p_half[x]);
                 }
                 arrive(&sh.p_full[x]);
