@@ -9,12 +9,13 @@
 //
 // Work.  The items' key tiles, laid end to end (with an allowance per item), are
 // cut into equal shares, one per CTA (one CTA per SM), wherever the cuts fall: a
-// share is a run of segments (item, key tiles).  An item cut into several segments leaves unnormalised sums
-// and their maxima in the workspace, and the combine kernel joins them in the
-// order of the segments.  So one long sequence, many short ones and any mixture
-// fill the GPU alike, and the result does not depend on timing.  Every CTA finds
-// its own share from the lengths (a sum over the sequences), which takes about a
-// microsecond; a separate planning kernel cost 4 to 25.
+// share is a run of segments (item, key tiles).  An item cut into several segments
+// leaves unnormalised sums and their maxima in the workspace, and the combine
+// kernel joins them in the order of the segments.  So one long sequence, many
+// short ones and any mixture fill the GPU alike, and the result does not depend on
+// timing.  Every CTA finds its own share from the lengths (a sum over the
+// sequences), which takes about a microsecond; a separate planning kernel cost 4 to
+// 25.
 //
 // A CTA (384 threads):
 //   warps 0-3, 4-7  two softmax groups, a thread per row

@@ -307,12 +307,13 @@ GDN2_API gdn2_status gdn2_recurrent_fwd(const void *q, const void *k, const void
                                         size_t workspace_bytes, void *stream);
 
 /*
- * Read the device-side status that the last gdn2_chunk_fwd or
- * gdn2_recurrent_fwd on this workspace wrote into *status: GDN2_OK,
- * GDN2_ERR_CU_SEQLENS, GDN2_ERR_TIMEOUT (a tensor-core kernel waited more
- * than 2 s on one of its own barriers and unwound), GDN2_ERR_RANGE (an fp16
- * intermediate was clipped) or, in a checked build only, GDN2_ERR_BOUNDS (an
- * index check failed); with any of the last three the outputs are invalid.
+ * Read the device-side status that the last gdn2_chunk_fwd,
+ * gdn2_recurrent_fwd or call of gdn2_attn.h on this workspace wrote into
+ * *status: GDN2_OK, GDN2_ERR_CU_SEQLENS, GDN2_ERR_PAGES (gdn2_attn.h),
+ * GDN2_ERR_TIMEOUT (a tensor-core kernel waited more than 2 s on one of its
+ * own barriers and unwound), GDN2_ERR_RANGE (an fp16 intermediate was
+ * clipped) or, in a checked build only, GDN2_ERR_BOUNDS (an index check
+ * failed); with any of the last three the outputs are invalid.
  * If several apply, the first in that order is reported.  This call
  * SYNCHRONISES `stream`.  Returns GDN2_ERR_CUDA if the copy fails.
  */
