@@ -5,17 +5,25 @@ key/value cache and the attention over it.
 Argument marshalling only, as in ``gdn2``: every step runs in the library's
 CUDA kernels, outputs and workspaces are allocated with torch when the caller
 does not pass them, and there is no CPU path.
+
+A decode step calls these functions with a few microseconds of GPU work per
+call.  So what depends on the tensors' metadata alone is worked out here, once
+per set of shapes, strides, dtypes and options (the checks and the dims struct,
+``_norm_rope_dims`` and its like), and the calls for known metadata are made by
+a compiled module (csrc/gdn2_attn_call.cpp).  Nothing is kept by address or
+content.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import math
+import os
 
 import torch
 
-from . import gdn2
-from .gdn2 import GDN2_OK, Gdn2Error, device_status  # noqa: F401  (status reader of these calls too)
+from . import build, gdn2
+from .gdn2 import Gdn2Error, device_status  # noqa: F401  (status reader of these calls too)
 
 EXPORTS = ("gdn2_attn_dims_init", "gdn2_qk_norm_rope", "gdn2_kv_append_workspace_bytes", "gdn2_kv_append",
            "gdn2_paged_attn_workspace_bytes", "gdn2_paged_attn_fwd")
@@ -34,11 +42,17 @@ class AttnDims(ctypes.Structure):
 
 
 _bound = None
+_call = None  # the compiled module, bound to the library
+
+
+def _raise(status, call):
+    raise Gdn2Error(status, call)
 
 
 def load():
-    """The library of ``gdn2.load()`` with these entry points' signatures set."""
-    global _bound
+    """The library of ``gdn2.load()`` with these entry points' signatures set,
+    and the compiled module bound to it."""
+    global _bound, _call
     lib = gdn2.load()
     if lib is not _bound:
         dims = ctypes.POINTER(AttnDims)
@@ -54,7 +68,15 @@ def load():
         lib.gdn2_paged_attn_workspace_bytes.restype = _sz
         lib.gdn2_paged_attn_fwd.argtypes = [_vp] * 6 + [_f32, _vp, _vp, dims, _vp, _sz, _vp]
         lib.gdn2_paged_attn_fwd.restype = ctypes.c_int
-        _bound = lib
+        if not os.path.exists(build.CALL):
+            raise RuntimeError("%s is not built; run __graft_entry__.build()" % os.path.basename(build.CALL))
+        spec = importlib.util.spec_from_file_location("gdn2_attn_call", build.CALL)
+        call = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(call)
+        call.bind(*(ctypes.cast(f, _vp).value for f in (lib.gdn2_qk_norm_rope, lib.gdn2_kv_append,
+                                                        lib.gdn2_paged_attn_workspace_bytes, lib.gdn2_paged_attn_fwd)),
+                  _raise)
+        _call, _bound = call, lib
     return lib
 
 
@@ -93,14 +115,6 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, trained_
     return f.to(device), rope_factor
 
 
-# A decode step calls these functions with a few microseconds of GPU work per call,
-# so what depends on the tensors' metadata alone (the checks, the dims struct, the
-# workspace size) is worked out once per set of shapes, strides and dtypes and kept
-# (`_norm_rope_plan` and its like, keyed by that metadata); a call then costs its
-# allocations and the library's launch.  Nothing is kept by address or content.
-_PLANS = 512
-
-
 def _rows(t):
     """Metadata of a strided tensor."""
     return None if t is None else (t.shape, t.stride(), t.dtype, t.is_cuda)
@@ -109,18 +123,6 @@ def _rows(t):
 def _flat(t):
     """Metadata of a tensor that has to be contiguous."""
     return None if t is None else (t.numel(), t.dtype, t.is_cuda and t.is_contiguous())
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):
-    def _stream(t, stream):
-        return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream
-else:
-    def _stream(t, stream):
-        return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
 
 
 def _code(*metas):
@@ -181,8 +183,9 @@ def _check_paged(k_cache, v_cache, table, lens, cu):
     return n, kc[:3], vc[:3], max(stride[0], size[1]), size[1], 1 if cu[1] == torch.int64 else 0
 
 
-@functools.lru_cache(maxsize=_PLANS)
-def _norm_rope_plan(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions, norm, interleaved, eps, rope_factor):
+def _norm_rope_dims(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions, norm, interleaved, eps, rope_factor):
+    q, k, q_out, k_out = _rows(q), _rows(k), _rows(q_out), _rows(k_out)
+    q_weight, k_weight, inv_freq, positions = _flat(q_weight), _flat(k_weight), _flat(inv_freq), _flat(positions)
     if len(q[0]) != 3:
         raise ValueError("q must be [tokens, heads, channels]")
     T, HQ, D = q[0]
@@ -197,10 +200,9 @@ def _norm_rope_plan(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions,
     elif k_out is not None:
         raise ValueError("k_out was given without k")
     rot, pos64 = _check_rope(norm, q, D, T, q_weight, k_weight, inv_freq, positions, True)
-    dims = AttnDims(T, 0, qs, ks, (0, 0), qo, ko, (0, 0, 0), (0, 0, 0), 0, 0, HQ, HK, D, 0, 0,
+    return AttnDims(T, 0, qs, ks, (0, 0), qo, ko, (0, 0, 0), (0, 0, 0), 0, 0, HQ, HK, D, 0, 0,
                     _code(q, k, q_out, k_out), 0, pos64, 1 if norm else 0, rot, 1 if interleaved else 0, 1, -1, eps,
                     rope_factor)
-    return ctypes.byref(dims), (T, HQ, D), (T, HK, D)
 
 
 def qk_norm_rope(q, k=None, positions=None, inv_freq=None, rope_factor=1.0, interleaved=False, norm=True,
@@ -216,24 +218,21 @@ def qk_norm_rope(q, k=None, positions=None, inv_freq=None, rope_factor=1.0, inte
     ``interleaved``.  q_out, k_out may be q, k (in place).  Returns (q_out,
     k_out).
     """
-    lib = load()
-    dims, q_shape, k_shape = _norm_rope_plan(_rows(q), _rows(k), _rows(q_out), _rows(k_out), _flat(q_weight),
-                                             _flat(k_weight), _flat(inv_freq), _flat(positions), bool(norm),
-                                             bool(interleaved), eps, rope_factor)
-    if q_out is None:
-        q_out = torch.empty(q_shape, dtype=q.dtype, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k_shape, dtype=k.dtype, device=k.device)
-    st = lib.gdn2_qk_norm_rope(q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-                               _ptr(positions), q_out.data_ptr(), _ptr(k_out), dims, _stream(q, stream))
-    if st != GDN2_OK:
-        raise Gdn2Error(st, "gdn2_qk_norm_rope")
-    return q_out, k_out
+    if _call is None:
+        load()
+    args = (q, k, positions, inv_freq, rope_factor, interleaved, norm, q_weight, k_weight, eps, q_out, k_out, stream)
+    r = _call.qk_norm_rope(*args)
+    if r is NotImplemented:
+        r = _call.qk_norm_rope(*args, bytes(_norm_rope_dims(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions,
+                                                            norm, interleaved, eps, rope_factor)))
+    return r
 
 
-@functools.lru_cache(maxsize=_PLANS)
-def _append_plan(q, k, v, q_out, k_cache, v_cache, table, lens, cu, q_weight, k_weight, inv_freq, positions, norm,
+def _append_dims(q, k, v, q_out, k_cache, v_cache, table, lens, cu, q_weight, k_weight, inv_freq, positions, norm,
                  interleaved, eps, rope_factor):
+    q, k, v, q_out, k_cache, v_cache, table = [_rows(t) for t in (q, k, v, q_out, k_cache, v_cache, table)]
+    lens, cu, q_weight, k_weight, inv_freq, positions = [
+        _flat(t) for t in (lens, cu, q_weight, k_weight, inv_freq, positions)]
     ks = _check_rows("k", k)
     T, HKV, D = k[0]
     vs = _check_rows("v", v, (T, HKV, D))
@@ -250,10 +249,9 @@ def _append_plan(q, k, v, q_out, k_cache, v_cache, table, lens, cu, q_weight, k_
     elif q_out is not None:
         raise ValueError("q_out was given without q")
     rot, pos64 = _check_rope(norm, k, D, T, q_weight, k_weight, inv_freq, positions, False)
-    dims = AttnDims(T, pages, qs, ks, vs, qo, (0, 0), kc, vc, ts, n, HQ, HKV, D, page, width,
+    return AttnDims(T, pages, qs, ks, vs, qo, (0, 0), kc, vc, ts, n, HQ, HKV, D, page, width,
                     _code(k, v, q, q_out, k_cache, v_cache), cu64, pos64, 1 if norm else 0, rot,
                     1 if interleaved else 0, 1, -1, eps, rope_factor)
-    return ctypes.byref(dims), (T, HQ, D)
 
 
 def append_kv(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q=None, positions=None, inv_freq=None,
@@ -271,39 +269,33 @@ def append_kv(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q=None, 
     the workspace reports a bad length, place or table entry.  Returns q_out
     (None without q).
     """
-    lib = load()
-    dims, q_shape = _append_plan(_rows(q), _rows(k), _rows(v), _rows(q_out), _rows(k_cache), _rows(v_cache),
-                                 _rows(block_table), _flat(kv_lens), _flat(cu_seqlens), _flat(q_weight),
-                                 _flat(k_weight), _flat(inv_freq), _flat(positions), bool(norm), bool(interleaved),
-                                 eps, rope_factor)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q_shape, dtype=q.dtype, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(64, dtype=torch.uint8, device=k.device)
-    st = lib.gdn2_kv_append(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-                            _ptr(positions), cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
-                            _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), dims, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream(k, stream))
-    if st != GDN2_OK:
-        raise Gdn2Error(st, "gdn2_kv_append")
-    return q_out
+    if _call is None:
+        load()
+    args = (k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q, positions, inv_freq, rope_factor, interleaved,
+            norm, q_weight, k_weight, eps, q_out, workspace, stream)
+    r = _call.append_kv(*args)
+    if r is NotImplemented:
+        r = _call.append_kv(*args, bytes(_append_dims(q, k, v, q_out, k_cache, v_cache, block_table, kv_lens,
+                                                      cu_seqlens, q_weight, k_weight, inv_freq, positions, norm,
+                                                      interleaved, eps, rope_factor)))
+    return r
 
 
-@functools.lru_cache(maxsize=_PLANS)
-def _attn_plan(q, k_cache, v_cache, table, lens, cu, out, lse, causal, window_left):
+def _attn_dims(q, k_cache, v_cache, table, lens, cu, out, lse, causal, window_left):
+    q, k_cache, v_cache, table, out = _rows(q), _rows(k_cache), _rows(v_cache), _rows(table), _rows(out)
+    lens, cu, lse = _flat(lens), _flat(cu), _flat(lse)
     qs = _check_rows("q", q)
     T, HQ, D = q[0]
     n, kc, vc, ts, width, cu64 = _check_paged(k_cache, v_cache, table, lens, cu)
     pages, page, HKV, dk = k_cache[0]
     if dk != D:
         raise ValueError("the cache's channels differ from q's")
-    os = (HQ * D, D) if out is None else _check_rows("out", out, (T, HQ, D))
+    out_stride = (HQ * D, D) if out is None else _check_rows("out", out, (T, HQ, D))
     if lse is not None:
         _check_flat("lse", lse, (torch.float32,), T * HQ)
-    dims = AttnDims(T, pages, qs, (0, 0), (0, 0), os, (0, 0), kc, vc, ts, n, HQ, HKV, D, page, width,
-                    _code(q, out, k_cache, v_cache), cu64, 0, 0, 0, 0, 1 if causal else 0, window_left, 0.0, 1.0)
-    ref = ctypes.byref(dims)
-    return ref, (T, HQ, D), (T, HQ), max(load().gdn2_paged_attn_workspace_bytes(ref), 64)
+    return AttnDims(T, pages, qs, (0, 0), (0, 0), out_stride, (0, 0), kc, vc, ts, n, HQ, HKV, D, page, width,
+                    _code(q, out, k_cache, v_cache), cu64, 0, 0, 0, 0, 1 if causal else 0,
+                    min(window_left, 2 ** 31 - 1), 0.0, 1.0)
 
 
 def paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale=None, causal=True, window_left=-1,
@@ -317,20 +309,12 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale=
     means 1/sqrt(D).  Returns out [T, HQ, D], or (out, lse [T, HQ] fp32) with
     ``return_lse``; a token with no key gets zeros and lse -inf.
     """
-    lib = load()
-    dims, shape, lse_shape, need = _attn_plan(_rows(q), _rows(k_cache), _rows(v_cache), _rows(block_table),
-                                              _flat(kv_lens), _flat(cu_seqlens), _rows(out), _flat(lse), bool(causal),
-                                              window_left)
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = lib.gdn2_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens.data_ptr(),
-                                 kv_lens.data_ptr(), block_table.data_ptr(), 0.0 if scale is None else scale,
-                                 out.data_ptr(), _ptr(lse), dims, workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(q, stream))
-    if st != GDN2_OK:
-        raise Gdn2Error(st, "gdn2_paged_attn_fwd")
-    return (out, lse) if return_lse else out
+    if _call is None:
+        load()
+    args = (q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale, causal, window_left, out, lse, return_lse,
+            workspace, stream)
+    r = _call.paged_attn_fwd(*args)
+    if r is NotImplemented:
+        r = _call.paged_attn_fwd(*args, bytes(_attn_dims(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, out, lse,
+                                                         causal, window_left)))
+    return r

@@ -616,3 +616,61 @@ def test_nothing_is_written_past_the_buffers(cuda_lib):
         buffers += [qo[0], out[0], lse[0], aws[0], ws[0]]
     for b in buffers:
         assert (b[:guard] == 0x5A).all() and (b[-guard:] == 0x5A).all()
+
+
+def test_calls_of_many_shapes_and_layouts(cuda_lib):
+    """More sets of metadata than are kept, repeats among them, and the same shapes in other layouts and dtypes."""
+    g = gen(41)
+    f, _ = attn.rope_frequencies(64)
+    q = normal(g, 600, 2, 64)
+    pos = torch.arange(600, device="cuda", dtype=torch.int32)
+    want, _ = attn.qk_norm_rope(q, None, pos, f)
+    for t in list(range(1, 600)) + [5, 599, 5]:
+        y, none = attn.qk_norm_rope(q[:t], None, pos[:t], f)
+        assert none is None and y.shape == (t, 2, 64) and y.is_contiguous() and torch.equal(y, want[:t])
+    for other in (q.transpose(0, 1).contiguous().transpose(0, 1), q.half(), torch.nn.Parameter(q), q[::2]):
+        n = other.shape[0]
+        for p in (pos[:n], pos[:n].long()):
+            y, _ = attn.qk_norm_rope(other, None, p, f)
+            assert y.dtype == other.dtype
+            close_rope(y, norm_rope(f64(other), p.tolist(), f.tolist()), "layout")
+    y, _ = attn.qk_norm_rope(q[:9], None, pos[:9], f, interleaved=True, eps=1e-2, rope_factor=2)
+    close_rope(y, norm_rope(f64(q[:9]), range(9), f.tolist(), None, True, True, 2.0, 1e-2), "options")
+
+
+def test_refusals_of_known_and_unknown_calls(cuda_lib):
+    from gated_deltanet_prefill_gb300.gdn2 import Gdn2Error
+    g = gen(42)
+    c = Cache(g, [4, 4], [14, 30], 16, 2, 64)
+    q, k, v = normal(g, 8, 4, 64), normal(g, 8, 2, 64), normal(g, 8, 2, 64)
+    f, _ = attn.rope_frequencies(64)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    for _ in range(2):  # the second time the metadata are known
+        attn.paged_attn_fwd(q, *c.args(), workspace=ws)
+        attn.append_kv(k, v, *c.args(), norm=False, workspace=ws)
+        for status, call in (
+                (8, lambda: attn.qk_norm_rope(q.float(), None)),
+                (2, lambda: attn.qk_norm_rope(q[..., :32].contiguous(), None)),
+                (4, lambda: attn.qk_norm_rope(q, None, q_out=torch.as_strided(q, (8, 4, 64), (0, 64, 1)))),
+                (5, lambda: attn.append_kv(k, v, *c.args(), workspace=ws[:32])),
+                (4, lambda: attn.append_kv(k, v, c.k, c.k, *c.args()[2:])),
+                (5, lambda: attn.paged_attn_fwd(q, *c.args(), workspace=ws[:64])),
+                (4, lambda: attn.paged_attn_fwd(q, *c.args(), out=q)),
+                (2, lambda: attn.paged_attn_fwd(q[:, :3], *c.args())),
+                (2, lambda: attn.paged_attn_fwd(q, *c.args(), causal=False, window_left=3))):
+            with pytest.raises(Gdn2Error) as e:
+                call()
+            assert e.value.status == status
+        for call in (lambda: attn.qk_norm_rope(q, k[:3]), lambda: attn.qk_norm_rope(q, None, None, f),
+                     lambda: attn.qk_norm_rope(q, None, torch.arange(8), f), lambda: attn.qk_norm_rope(q.cpu(), None),
+                     lambda: attn.qk_norm_rope(q, None, norm=False, q_weight=q[0, 0]),
+                     lambda: attn.append_kv(k, v, c.k, c.v, c.table, c.lens[:1], c.cu),
+                     lambda: attn.append_kv(k, v[:, :1], *c.args()),
+                     lambda: attn.paged_attn_fwd(q, c.k, c.v, c.table.long(), c.lens, c.cu),
+                     lambda: attn.paged_attn_fwd(q, c.k, c.v[:, :8], c.table, c.lens, c.cu)):
+            with pytest.raises(ValueError):
+                call()
+        with pytest.raises((TypeError, AttributeError)):
+            attn.qk_norm_rope([1.0], None)
+        with pytest.raises(TypeError):
+            attn.qk_norm_rope(q, None, eps="small")
