@@ -15,6 +15,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -151,11 +152,27 @@ void *data(const at::Tensor *t) { return t ? t->data_ptr() : nullptr; }
 at::Tensor empty(at::IntArrayRef size, at::ScalarType dtype, const at::Tensor &like) {
     return at::Tensor(at::detail::empty_cuda(size, dtype, like.device(), std::nullopt));
 }
-// The stream given (an address), or the current one of the tensor's device.
-void *stream_of(PyObject *o, const at::Tensor &t) {
-    if (o != Py_None) return PyLong_AsVoidPtr(o);
-    return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
-}
+// Where the call runs: the stream given (an address), or the current one of the
+// tensor's device.
+struct Stream {
+    void *handle = nullptr;
+    bool other = false;  // not the current one
+    c10::DeviceIndex device;
+    Stream(PyObject *o, const at::Tensor &t) : device(t.device().index()) {
+        void *const current = c10::cuda::getCurrentCUDAStream(device).stream();
+        handle = o == Py_None ? current : PyLong_AsVoidPtr(o);
+        other = handle != current;
+    }
+    // Memory made here belongs to the current stream: where the call runs on another,
+    // it must not be handed out again before that one has passed this point.
+    void keep(std::initializer_list<const at::Tensor *> made) const {
+        if (!other) return;
+        for (const at::Tensor *t : made)
+            if (t->defined())
+                c10::cuda::CUDACachingAllocator::recordStream(
+                    t->storage().data_ptr(), c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), device));
+    }
+};
 PyObject *failed(gdn2_status st, const char *what) {
     PyObject *r = PyObject_CallFunction(raise_error, "is", static_cast<int>(st), what);
     Py_XDECREF(r);
@@ -189,7 +206,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Plan plan;
     if (!find(plans, key, args, plan)) return unknown();
     const gdn2_attn_dims &d = plan.dims;
-    void *const s = stream_of(stream, *q);
+    const Stream s(stream, *q);
     if (PyErr_Occurred()) return nullptr;
     at::Tensor qo, ko;
     if (!q_out) q_out = &(qo = empty({d.T_tot, d.HQ, d.D}, q->scalar_type(), *q));
@@ -197,8 +214,9 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *const p[] = {data(q), data(k), data(q_weight), data(k_weight), data(inv_freq), data(positions), data(q_out), data(k_out)};
     gdn2_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = qk_norm_rope_fn(p[0], p[1], p[2], p[3], static_cast<const double *>(p[4]), p[5], p[6], p[7], &d, s);
+    st = qk_norm_rope_fn(p[0], p[1], p[2], p[3], static_cast<const double *>(p[4]), p[5], p[6], p[7], &d, s.handle);
     Py_END_ALLOW_THREADS
+    s.keep({&qo, &ko});
     if (st != GDN2_OK) return failed(st, "gdn2_qk_norm_rope");
     PyObject *r0 = result(a[10], qo), *r1 = k ? result(a[11], ko) : Py_NewRef(Py_None);
     return Py_BuildValue("(NN)", r0, r1);
@@ -229,7 +247,7 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Plan plan;
     if (!find(plans, key, args, plan)) return unknown();
     const gdn2_attn_dims &d = plan.dims;
-    void *const s = stream_of(stream, *k);
+    const Stream s(stream, *k);
     if (PyErr_Occurred()) return nullptr;
     at::Tensor qo, ws;
     if (!q_out && q) q_out = &(qo = empty({d.T_tot, d.HQ, d.D}, q->scalar_type(), *q));
@@ -241,8 +259,9 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Py_BEGIN_ALLOW_THREADS
     st = kv_append_fn(p[0], p[1], p[2], p[3], p[4], static_cast<const double *>(p[5]), p[6], p[7],
                       static_cast<const int32_t *>(p[8]), static_cast<const int32_t *>(p[9]), p[10], p[11], p[12], &d, p[13],
-                      bytes, s);
+                      bytes, s.handle);
     Py_END_ALLOW_THREADS
+    s.keep({&qo, &ws});
     if (st != GDN2_OK) return failed(st, "gdn2_kv_append");
     if (!q) Py_RETURN_NONE;
     return result(a[16], qo);
@@ -273,7 +292,7 @@ PyObject *paged_attn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Plan plan;
     if (!find(plans, key, args, plan)) return unknown();
     const gdn2_attn_dims &d = plan.dims;
-    void *const s = stream_of(stream, *q);
+    const Stream s(stream, *q);
     if (PyErr_Occurred()) return nullptr;
     at::Tensor o, l, ws;
     if (!out) out = &(o = empty({d.T_tot, d.HQ, d.D}, q->scalar_type(), *q));
@@ -284,8 +303,9 @@ PyObject *paged_attn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     gdn2_status st;
     Py_BEGIN_ALLOW_THREADS
     st = paged_attn_fn(p[0], p[1], p[2], p[3], static_cast<const int32_t *>(p[4]), static_cast<const int32_t *>(p[5]),
-                       static_cast<float>(scale), p[6], static_cast<float *>(p[7]), &d, p[8], bytes, s);
+                       static_cast<float>(scale), p[6], static_cast<float *>(p[7]), &d, p[8], bytes, s.handle);
     Py_END_ALLOW_THREADS
+    s.keep({&o, &l, &ws});
     if (st != GDN2_OK) return failed(st, "gdn2_paged_attn_fwd");
     PyObject *r = result(a[9], o);
     if (!return_lse) return r;

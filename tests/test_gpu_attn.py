@@ -674,3 +674,26 @@ def test_refusals_of_known_and_unknown_calls(cuda_lib):
             attn.qk_norm_rope([1.0], None)
         with pytest.raises(TypeError):
             attn.qk_norm_rope(q, None, eps="small")
+
+
+def test_call_on_a_stream_other_than_the_current_one(cuda_lib):
+    """Memory made for a call on a given stream is not handed out while that stream still waits."""
+    g = gen(43)
+    c = Cache(g, [1, 40, 1], [70, 0, 130], 16, 2, 128)
+    q, k, v = normal(g, 42, 8, 128), normal(g, 42, 2, 128), normal(g, 42, 2, 128)
+    f, _ = attn.rope_frequencies(128)
+    qo = attn.append_kv(k, v, *c.args(), q=q, inv_freq=f)
+    want, wl = attn.paged_attn_fwd(qo, *c.args(), return_lse=True)
+    size = attn.load().gdn2_paged_attn_workspace_bytes
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    out, lse = attn.paged_attn_fwd(qo, *c.args(), return_lse=True, stream=side.cuda_stream)
+    x, _ = attn.qk_norm_rope(q, None, norm=False, stream=side.cuda_stream)
+    dims = attn._attn_dims(qo, *c.args(), None, None, True, -1)
+    blocks = [torch.full((size(dims),), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.current_stream().synchronize()
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl) and torch.equal(x, q)
+    assert all((b == 255).all() for b in blocks)
