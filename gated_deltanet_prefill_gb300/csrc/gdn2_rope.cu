@@ -14,8 +14,8 @@
 // interleaved one the partner is in the lane) and 16 multiply-adds.
 //
 // Bound by memory: 32768 tokens of 32 + 32 heads (half of each head rotated) take
-// 179 us, 6.00 TB/s of the 6.78 that a copy reaches; the append of 34997 tokens of
-// 32 + 32 + 32 heads to pages of 16 takes 266 us, 6.46 TB/s.  The packed fp32
+// 178 us, 6.03 TB/s of the 6.78 that a copy reaches; the append of 34997 tokens of
+// 32 + 32 + 32 heads to pages of 16 takes 263 us, 6.54 TB/s.  The packed fp32
 // instructions keep the issue slots below what the loads need.  A warp takes all
 // heads of a token when there are tokens enough to fill the GPU, and a slice of
 // them otherwise, so that a decode step is one row group per warp (128 tokens of
@@ -29,15 +29,18 @@ namespace {
 using namespace tc;
 
 constexpr int kWarps = 4;    // warps per block
-constexpr int kUnroll = 4;   // row groups in flight per warp
+constexpr int kUnroll = 4;
 // Blocks per SM that the registers are cut for (72 a thread; a few of the
 // coefficients spill).  Measured on 32768 tokens of 64 heads and on the append of
 // 34997 tokens of 96: 200 and 288 us uncut (92 registers, 5 blocks), 187 and 269
 // with 6, 179 and 266 with 7, 179 and 268 with 8; 2 groups in flight at 8 blocks
 // 192 and 290, 8 groups at 4 blocks 205 and 284.
 constexpr int kMinBlocks = 7;
-// Resident warps that the slicing aims at, per SM.
-constexpr int kWarpsPerSm = 32;
+// Warps per SM that the slicing aims at: every slice of a token forms the angles
+// (and finds the page) again, so not all 28 that fit.  4099 tokens of 20 heads, 128 of 40,
+// the append of 4600 tokens of 20 rows and of 128 of 48: 7.9, 4.1, 9.1 and 5.7 us with
+// 32; 6.3, 3.8, 7.9 and 4.9 with 16 (and with 12).
+constexpr int kWarpsPerSm = 16;
 
 // Angle per position as a fraction of a turn in units of 2^-64 turns: f / (2
 // pi) * 2^64 modulo 2^64, from the double's bits (integers only: double
@@ -203,6 +206,23 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks) gdn2_rope_kernel(cons
     const int r0 = static_cast<int>(warp - t * slices) * rows_per_slice;
     const int r1 = min(r0 + rows_per_slice, p.HQ + p.HK + p.HV);
 
+    // The first rows are asked for at once: what comes before their use, the place in
+    // the cache and the angles, is a chain of loads of its own.
+    uint4 u[kUnroll];
+    auto load = [&](int h0, int hi, const bf16 *x, int64_t sx) {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int h = h0 + i * R + sub;
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (h < hi) u[i] = *reinterpret_cast<const uint4 *>(x + h * sx + 8 * c);
+        }
+    };
+    const int k0 = p.HQ, v0 = p.HQ + p.HK;
+    if (r0 < k0)
+        load(r0, min(r1, k0), p.q + t * p.sq_t, p.sq_h);
+    else if (r0 < v0)
+        load(r0 - k0, min(r1, v0) - k0, p.k + t * p.sk_t, p.sk_h);
+
     Place at = {0, 0, 0, true};
     if (PAGED) {
         at = place_of(p, t, lane);
@@ -230,7 +250,7 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks) gdn2_rope_kernel(cons
     }
 
     // rows [lo, hi) of one kind: queries or keys
-    auto rows = [&](int lo, int hi, const bf16 *x, int64_t sx, bf16 *y, int64_t sy, const bf16 *w) {
+    auto rows = [&](int lo, int hi, const bf16 *x, int64_t sx, bf16 *y, int64_t sy, const bf16 *w, bool loaded) {
         if (lo >= hi) return;
         uint64_t A[4], B[4];  // of channels 2 e and 2 e + 1
         {
@@ -249,13 +269,8 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks) gdn2_rope_kernel(cons
         }
         const int src = lane - c + partner;
         for (int h0 = lo; h0 < hi; h0 += R * kUnroll) {
-            uint4 u[kUnroll];
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const int h = h0 + i * R + sub;
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (h < hi) u[i] = *reinterpret_cast<const uint4 *>(x + h * sx + 8 * c);
-            }
+            if (!loaded) load(h0, hi, x, sx);
+            loaded = false;
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 if (h0 + i * R >= hi) break;  // the same for all lanes
@@ -301,17 +316,15 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks) gdn2_rope_kernel(cons
             }
         }
     };
-    rows(r0, min(r1, p.HQ), p.q + t * p.sq_t, p.sq_h, p.q_out + t * p.sqo_t, p.sqo_h, p.q_weight);
-    const int k0 = p.HQ, v0 = p.HQ + p.HK;
+    rows(r0, min(r1, p.HQ), p.q + t * p.sq_t, p.sq_h, p.q_out + t * p.sqo_t, p.sqo_h, p.q_weight, true);
     rows(max(r0, k0) - k0, min(r1, v0) - k0, p.k + t * p.sk_t, p.sk_h,
          PAGED ? p.k_cache + at.page * p.skc[0] + at.slot * p.skc[1] : p.k_out + t * p.sko_t,
-         PAGED ? p.skc[2] : p.sko_h, p.k_weight);
+         PAGED ? p.skc[2] : p.sko_h, p.k_weight, r0 >= k0);
     if (PAGED) {
         const bf16 *x = p.v + t * p.sv_t;
         bf16 *y = p.v_cache + at.page * p.svc[0] + at.slot * p.svc[1];
         const int hi = r1 - v0;
         for (int h0 = max(r0, v0) - v0 + sub; h0 < hi; h0 += R * kUnroll) {
-            uint4 u[kUnroll];
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i)
                 if (h0 + i * R < hi) u[i] = *reinterpret_cast<const uint4 *>(x + (h0 + i * R) * p.sv_h + 8 * c);
