@@ -95,6 +95,7 @@ struct KernelParams {
     int tt;                      // tokens per row tile: 128 / G
     int granule;                 // keys per TMA box
     int kpos[3], vpos[3];        // coordinate (1 .. 3) of page, token, head in the tensor maps
+    int ctas;                    // of the main kernel
     int q_map;                   // tq is set: the queries come by TMA
     CUtensorMap tk, tv, tq;
 };
@@ -1261,78 +1262,116 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
 }
 
 // ---------------------------------------------------------------- combine
-// Rows of the items that were cut: a warp per row,
-//   M = max_i m_i,  L = sum_i 2^(m_i - M) l_i,  o = sum_i 2^(m_i - M) o_i / L.
-// The first block also gathers the CTAs' flags into the status words.
-constexpr int kJoinRows = 16;  // rows of a block: 8 warps, 4 rows each
+// Rows of the items that were cut, pieces in order, kPieces at a time:
+//   M' = max(M, m_i),  (L, o) <- 2^(M - M') (L, o) + sum_i 2^(m_i - M') (l_i, o_i);  o / L.
+// Bound by latency: joints, pieces and store are a chain of loads, in code that runs
+// once or twice, so at the rate of instruction fetch.  So: every block reads all
+// joints and finds its rows, in a grid that is resident at once, and the code is
+// one row of D / 4 lanes with four pieces under way.  Measured on 7 windowed chunks
+// (1200 rows cut), one token, and one token over 131072 keys, whole call: 26.3,
+// 13.0 and 90.6 us; four rows of two pieces side by side 26.3, 13.4 and 91.5; two
+// rows 27.1, 13.7 and 93.2; a block per 16 rows, before, 30.1, 13.1 and 91.9.
+constexpr int kJoinWarps = 8, kJoinBlocks = 4;  // warps of a block, blocks per SM
+constexpr int kPieces = 4;
 
+// The first block also gathers the CTAs' flags into the status words.
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) gdn2_attn_combine_kernel(const __grid_constant__ KernelParams p) {
-    constexpr int E = D / 32;  // channels of a lane
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks) gdn2_attn_combine_kernel(const __grid_constant__ KernelParams p) {
+    constexpr int RW = 128 / D;  // rows of a warp
+    __shared__ Joint joints[kMaxCtas];
+    __shared__ int upto[kMaxCtas];  // tasks of the joints up to each, a task per warp
+    __shared__ int sums[kJoinWarps];
     const AttnParams &a = p.a;
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+    const int sub = lane / (D / 4), ch = lane % (D / 4) * 4;  // row and channels of this lane
+    const uint32_t inv_g = 65536u / a.G + 1;
+    static_assert(kMaxCtas <= 32 * kJoinWarps, "a joint per thread");
     pdl_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && wp == 0) {
-        int f = 0;
-        for (int c = lane; c < static_cast<int>(gridDim.x); c += 32) f |= p.flags[c];
-        f = __reduce_or_sync(0xffffffffu, f);
-        if (lane < 8)
-            a.status[lane] = lane == 0   ? f & kBadCu ? GDN2_ERR_CU_SEQLENS : f & kBadPages ? GDN2_ERR_PAGES : GDN2_OK
-                             : lane == 2 ? f & kTimeout ? GDN2_ERR_TIMEOUT : GDN2_OK
-                                         : 0;
+    Joint j = {};
+    if (tid < p.ctas) j = p.joint[tid];
+    int tasks = 0;
+    if (j.more > 0) {
+        const int rows = j.ntok > p.tt ? kTile + (j.ntok - p.tt) * a.G : j.ntok * a.G;
+        tasks = (rows + RW - 1) / RW;
     }
-    const Joint j = p.joint[blockIdx.x];
-    if (j.more <= 0) return;
-    for (int i = wp; i < kJoinRows; i += 8) {
-        const int r = blockIdx.y * kJoinRows + i, x = r / kTile, rr = r % kTile;
-        const int tk = rr / a.G, tok = x * p.tt + tk, hd = rr - tk * a.G;
-        if (tk >= p.tt || tok >= j.ntok) continue;
-        auto at = [&](int k) {
-            return static_cast<int64_t>(k == 0 ? j.slot : 2 * (static_cast<int>(blockIdx.x) + k)) * 2 * kTile + r;
-        };
-        float M = -INFINITY;
-        for (int k = lane; k <= j.more; k += 32) M = fmaxf(M, p.part_ml[at(k)].x);
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float base = M == -INFINITY ? 0.f : M;
-        float L = 0.f, acc[E];
+    int x = tasks;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int k0 = 0; k0 <= j.more; k0 += 32) {
-            float w = 0.f, l = 0.f;
-            if (k0 + lane <= j.more) {
-                const float2 ml = p.part_ml[at(k0 + lane)];
-                w = ex2(ml.x - base);
-                l = w * ml.y;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[wp] = x;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+        if (i < wp) x += sums[i];
+        total += sums[i];
+    }
+    if (tid < kMaxCtas) {
+        joints[tid] = j;
+        upto[tid] = x;
+    }
+    __syncthreads();
+    for (int task = blockIdx.x * kJoinWarps + wp; task < total; task += gridDim.x * kJoinWarps) {
+        int cta = 0;  // the first joint whose tasks end past this one
+        for (int base = 0; base < kMaxCtas; base += 32) {
+            const int i = base + lane;
+            cta += __popc(__ballot_sync(0xffffffffu, i < kMaxCtas && upto[i] <= task));
+        }
+        const Joint &g = joints[cta];
+        const int row = (task - (cta > 0 ? upto[cta - 1] : 0)) * RW + sub;
+        // the row's token, if it has one, and head
+        const int tile = row / kTile, in = row % kTile, tk = static_cast<int>((in * inv_g) >> 16), tok = tile * p.tt + tk;
+        if (tk >= p.tt || tok >= g.ntok) continue;  // (no collective operation follows in this round)
+        float M = -INFINITY, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 <= g.more; k0 += kPieces) {
+            float2 ml[kPieces];
+            float4 o[kPieces];
+            float top = M;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                ml[i] = make_float2(-INFINITY, 0.f);
+                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + i > g.more) continue;
+                const int64_t at = static_cast<int64_t>(k0 + i == 0 ? g.slot : 2 * (cta + k0 + i)) * 2 * kTile + row;
+                ml[i] = p.part_ml[at];
+                o[i] = *reinterpret_cast<const float4 *>(p.part_o + at * D + ch);
             }
-            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            L += l;
-            const int cnt = min(32, j.more + 1 - k0);
-#pragma unroll 4
-            for (int k = 0; k < cnt; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                const float *o = p.part_o + at(k0 + k) * D + lane * E;
-                if (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(o);
-                    acc[0] += wk * v.x; acc[1] += wk * v.y; acc[E - 2] += wk * v.z; acc[E - 1] += wk * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(o);
-                    acc[0] += wk * v.x; acc[1] += wk * v.y;
-                }
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) top = fmaxf(top, ml[i].x);
+            const float base = top == -INFINITY ? 0.f : top, f = ex2(M - base);
+            M = top;
+            L *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const float w = ex2(ml[i].x - base);
+                L += w * ml[i].y;
+                acc.x += w * o[i].x;
+                acc.y += w * o[i].y;
+                acc.z += w * o[i].z;
+                acc.w += w * o[i].w;
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int head = j.h * a.G + hd;
-        const int64_t tok_row = static_cast<int64_t>(j.tok0) + tok;
-        bf16 *o = a.out + tok_row * a.so_t + head * a.so_h + lane * E;
-        uint32_t w[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e)
-            w[e] = F16 ? pack_f16_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv) : pack_bf2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        if (E == 4)
-            *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[E / 2 - 1]);
-        else
-            *reinterpret_cast<uint32_t *>(o) = w[0];
-        if (a.lse && lane == 0) a.lse[tok_row * a.HQ + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        const int64_t at = static_cast<int64_t>(g.tok0) + tok;
+        const int head = g.h * a.G + in - tk * a.G;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + at * a.so_t + head * a.so_h + ch) =
+            F16 ? make_uint2(pack_f16_rn(acc.x, acc.y), pack_f16_rn(acc.z, acc.w))
+                : make_uint2(pack_bf2(acc.x, acc.y), pack_bf2(acc.z, acc.w));
+        if (a.lse && ch == 0) a.lse[at * a.HQ + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+    if (blockIdx.x == 0 && wp == kJoinWarps - 1) {
+        int f = 0;
+        for (int c = lane; c < p.ctas; c += 32) f |= p.flags[c];
+        f = __reduce_or_sync(0xffffffffu, f);
+        if (lane < 8)
+            a.status[lane] = lane == 0   ? f & kBadCu ? GDN2_ERR_CU_SEQLENS : f & kBadPages ? GDN2_ERR_PAGES : GDN2_OK
+                               : lane == 2 ? f & kTimeout ? GDN2_ERR_TIMEOUT : GDN2_OK
+                                           : 0;
     }
 }
 
@@ -1405,7 +1444,7 @@ cudaError_t launch(const KernelParams &p, int ctas, cudaStream_t s) {
     kern<<<ctas, kThreads, Cfg<D>::kSmem, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_chained(gdn2_attn_combine_kernel<D, F16>, dim3(ctas, 2 * kTile / kJoinRows), dim3(256), 0, s, p);
+    return launch_chained(gdn2_attn_combine_kernel<D, F16>, dim3(kJoinBlocks * ctas), dim3(32 * kJoinWarps), 0, s, p);
 }
 
 }  // namespace
@@ -1424,6 +1463,7 @@ cudaError_t launch_paged_attn(const AttnParams &a, const gdn2_attn_dims &d, int 
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.scale_log2 = a.scale * kLog2e;
+    p.ctas = ctas;
     p.tt = kTile / a.G;
     p.granule = 8;
     while (p.granule < kTile && a.page_size % (2 * p.granule) == 0) p.granule *= 2;
