@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
         const int x = wp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(wp & 3) << 21;  // TMEM lane of the warp's first row
         const uint32_t inv_g = 65536u / a.G + 1;                     // r / G for r < 128
-        const float sl2 = p.scale_log2, slack = 8.f / sl2;
+        const float sl2 = p.scale_log2, slack = fminf(8.f / sl2, 1e38f);
         const int my_tok = static_cast<int>((row * inv_g) >> 16), my_head = row - my_tok * a.G;
         // A group signals with one arrival per warp: 128 arrivals on one barrier
         // take their turns, which the products waited for.

@@ -697,3 +697,15 @@ def test_call_on_a_stream_other_than_the_current_one(cuda_lib):
     side.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, wl) and torch.equal(x, q)
     assert all((b == 255).all() for b in blocks)
+
+
+def test_attention_smallest_scale(cuda_lib):
+    """A scale near the smallest normal number: every key weighs the same."""
+    g = gen(44)
+    c = Cache(g, [2, 70], [300, 60], 16, 2, 64)
+    q = normal(g, 72, 4, 64)
+    for scale in (2e-38, 1e-30):
+        out, lse = attn.paged_attn_fwd(q, *c.args(), scale=scale, return_lse=True)
+        check_attn(q, c, out, lse, scale=scale)
+    out, lse = attn.paged_attn_fwd(q, *c.args(), scale=2e-38, window_left=3, return_lse=True)
+    check_attn(q, c, out, lse, scale=2e-38, window=3)
