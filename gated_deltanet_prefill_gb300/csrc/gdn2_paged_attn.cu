@@ -248,6 +248,7 @@ struct Share {
 // (flags and left zero).
 __device__ void find_share(const AttnParams &a, int tokens, Share &s) {
     const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+    const int parts = min(kThreads / 32, (a.N + 31) / 32);  // warps with sequences
     int flags = 0;
     if (tid == 0 && (a.N > 0 ? cu_of(a.cu, a.cu64, 0) != 0 || cu_of(a.cu, a.cu64, a.N) != a.T : a.T != 0)) flags = kBadCu;
     // cost of the sequence, and its inclusive sum over the warp
@@ -270,8 +271,8 @@ __device__ void find_share(const AttnParams &a, int tokens, Share &s) {
         if (flags) atomicOr(&s.flags, flags);
         __syncthreads();
         before = total;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) total += s.part[i];
+#pragma unroll 1
+        for (int i = 0; i < parts; ++i) total += s.part[i];
         if (base + kThreads < a.N) __syncthreads();
     }
     const bool one_round = a.N <= kThreads;
@@ -289,8 +290,8 @@ __device__ void find_share(const AttnParams &a, int tokens, Share &s) {
             __syncthreads();
         }
         long long from = before;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < parts; ++i) {
             if (i < wp) from += s.part[i];
             before += s.part[i];
         }
