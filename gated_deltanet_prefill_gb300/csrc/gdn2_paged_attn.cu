@@ -106,7 +106,9 @@ struct KernelParams {
     float2 *part_ml;             // [2 kMaxCtas][256] (log2-scaled maximum, sum)
     float scale_log2;
     int tt;                      // tokens per row tile: 128 / G
-    int granule;                 // keys per TMA box
+    int granule, granule_log2;   // keys per TMA box
+    uint32_t page_mul;           // key / page_size = umulhi(key, page_mul) >> page_shift
+    int page_shift;
     int kpos[3], vpos[3];        // coordinate (1 .. 3) of page, token, head in the tensor maps
     int ctas;                    // of the main kernel
     int q_map;                   // tq is set: the queries come by TMA
@@ -280,7 +282,12 @@ __device__ void find_share(const AttnParams &a, int tokens, Share &s) {
     if (s.flags || total == 0) return;
     const long long shares = min(total, static_cast<long long>(gridDim.x));
     if (blockIdx.x >= shares) return;
-    const long long begin = div_by(total * blockIdx.x, shares), end = div_by(total * (blockIdx.x + 1), shares);
+    // (a tile each needs no division, which takes 200 cycles)
+    long long begin = blockIdx.x, end = begin + 1;
+    if (total > shares) {
+        begin = div_by(total * begin, shares);
+        end = div_by(total * end, shares);
+    }
     before = 0;
     for (int base = 0; base < a.N; base += kThreads) {
         if (!one_round) {
@@ -331,7 +338,7 @@ struct Walk {
         }
     }
 
-    __device__ void enter() { items = (q.fresh + tokens - 1) / tokens; }
+    __device__ void enter() { items = q.fresh <= tokens ? 1 : (q.fresh + tokens - 1) / tokens; }
     __device__ Walk(const AttnParams &a_, int tokens_, const Share &s) : a(a_), tokens(tokens_) {
         left = s.left;
         first = true;
@@ -655,21 +662,22 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
         bool ok = true;
     };
     auto load_tiles = [&](Loader &ld, const Segment &g, bool is_v, auto at, auto ahead) {
-        const int gran = p.granule, per = kTile / gran;     // granules of a tile
-        const int batch = 32 / per;                         // tiles whose table entries one load fetches
+        // (a division takes 100 to 200 cycles, and these stand before the first copy)
+        const int gran = p.granule, per_log2 = 7 - p.granule_log2, per = 1 << per_log2;  // granules of a tile
+        const int batch = 32 >> per_log2;                   // tiles whose table entries one load fetches
         const int my_gr = lane / NB, my_cb = lane % NB;     // this lane's granule and channel block
         const int tiles = g.hi - g.lo;
         const int *row = a.table + static_cast<int64_t>(g.seq) * a.table_stride;
         const int *pos = is_v ? p.vpos : p.kpos;
         // page and slot of this lane's granule of the batch that starts at tile t
         auto fetch = [&](int t) {
-            t += lane / per;
+            t += lane >> per_log2;
             int2 e = make_int2(0, 0);
-            const int64_t key = static_cast<int64_t>(t) * kTile + (lane % per) * gran;
+            const int64_t key = static_cast<int64_t>(t) * kTile + (lane & (per - 1)) * gran;
             if (t < g.hi && key + gran <= g.begin) {
                 e.x = static_cast<int>(a.num_pages);  // before the window, where the page may be gone: zeros
             } else if (t < g.hi && key < g.end) {
-                const int col = static_cast<int>(key) / a.page_size;
+                const int col = static_cast<int>(__umulhi(static_cast<uint32_t>(key), p.page_mul) >> p.page_shift);
                 e = make_int2(row[col], static_cast<int>(key) - col * a.page_size);
                 if (e.x < 0 || e.x >= a.num_pages) {
                     e.x = static_cast<int>(a.num_pages);  // past the tensor: the box reads zeros
@@ -686,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             const uint32_t load = ld.base + at(i);
             const int st = static_cast<int>(load % C::kStages);
             const int left = min(kTile, g.end - (g.lo + i) * kTile);  // rows that count
-            const int grans = (left + gran - 1) / gran;
+            const int grans = (left + gran - 1) >> p.granule_log2;
             ld.ok = ld.ok && warp_wait(&empty[st], ((load / C::kStages) & 1) ^ 1);
             if (!ld.ok) return;
             const bool patch = is_v && (left < kTile || skip > 0);
@@ -1480,7 +1488,14 @@ cudaError_t launch_paged_attn(const AttnParams &a, const gdn2_attn_dims &d, int 
     p.ctas = ctas;
     p.tt = kTile / a.G;
     p.granule = 8;
-    while (p.granule < kTile && a.page_size % (2 * p.granule) == 0) p.granule *= 2;
+    p.granule_log2 = 3;
+    while (p.granule < kTile && a.page_size % (2 * p.granule) == 0) p.granule *= 2, ++p.granule_log2;
+    // floor(k / d) = floor(k m / 2^(31 + l)) for k < 2^31, with 2^(l - 1) < d <= 2^l and
+    // m = ceil(2^(31 + l) / d), which is at most 2^32 - 1
+    int l2 = 3;
+    while ((1ll << l2) < a.page_size) ++l2;
+    p.page_mul = static_cast<uint32_t>(((1ull << (31 + l2)) + a.page_size - 1) / a.page_size);
+    p.page_shift = l2 - 1;
     if (a.T > 0 && (!encode_cache(&p.tk, p.kpos, a.k_cache, a, a.skc, d.D, f16, p.granule) ||
                     !encode_cache(&p.tv, p.vpos, a.v_cache, a, a.svc, d.D, f16, p.granule)))
         return cudaErrorInvalidValue;
