@@ -351,6 +351,10 @@ struct Walk {
         enter();
         h = static_cast<int>(div_by(s.in_seq, s.cost));
         long long at = s.in_seq - h * s.cost;
+        if (items == 1) {
+            off = static_cast<int>(at);
+            return;
+        }
         // the item that holds tile `at` of the head
         const int lane = threadIdx.x & 31;
         if (items > 32 && closed_form(a, q.len, q.fresh)) {
@@ -673,12 +677,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
         auto fetch = [&](int t) {
             t += lane >> per_log2;
             int2 e = make_int2(0, 0);
-            const int64_t key = static_cast<int64_t>(t) * kTile + (lane & (per - 1)) * gran;
+            const int key = t * kTile + (lane & (per - 1)) * gran;
             if (t < g.hi && key + gran <= g.begin) {
                 e.x = static_cast<int>(a.num_pages);  // before the window, where the page may be gone: zeros
             } else if (t < g.hi && key < g.end) {
-                const int col = static_cast<int>(__umulhi(static_cast<uint32_t>(key), p.page_mul) >> p.page_shift);
-                e = make_int2(row[col], static_cast<int>(key) - col * a.page_size);
+                const int col = static_cast<int>(__umulhi(key, p.page_mul) >> p.page_shift);
+                e = make_int2(row[col], key - col * a.page_size);
                 if (e.x < 0 || e.x >= a.num_pages) {
                     e.x = static_cast<int>(a.num_pages);  // past the tensor: the box reads zeros
                     atomicOr(&sh.share.flags, kBadPages);
