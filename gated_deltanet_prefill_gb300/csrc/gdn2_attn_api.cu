@@ -289,6 +289,7 @@ gdn2_status gdn2_kv_append(const void *q, const void *k, const void *v, const vo
     p.num_pages = d.num_pages;
     p.N = d.N;
     p.page_size = d.page_size;
+    p.page = divisor(d.page_size);
     p.max_pages = d.max_pages;
     p.status = static_cast<int *>(workspace);
     cudaGetLastError();

@@ -107,8 +107,7 @@ struct KernelParams {
     float scale_log2;
     int tt;                      // tokens per row tile: 128 / G
     int granule, granule_log2;   // keys per TMA box
-    uint32_t page_mul;           // key / page_size = umulhi(key, page_mul) >> page_shift
-    int page_shift;
+    Divisor page;                // page_size
     int kpos[3], vpos[3];        // coordinate (1 .. 3) of page, token, head in the tensor maps
     int ctas;                    // of the main kernel
     int q_map;                   // tq is set: the queries come by TMA
@@ -681,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
             if (t < g.hi && key + gran <= g.begin) {
                 e.x = static_cast<int>(a.num_pages);  // before the window, where the page may be gone: zeros
             } else if (t < g.hi && key < g.end) {
-                const int col = static_cast<int>(__umulhi(key, p.page_mul) >> p.page_shift);
+                const int col = quotient(key, p.page);
                 e = make_int2(row[col], key - col * a.page_size);
                 if (e.x < 0 || e.x >= a.num_pages) {
                     e.x = static_cast<int>(a.num_pages);  // past the tensor: the box reads zeros
@@ -1494,12 +1493,7 @@ cudaError_t launch_paged_attn(const AttnParams &a, const gdn2_attn_dims &d, int 
     p.granule = 8;
     p.granule_log2 = 3;
     while (p.granule < kTile && a.page_size % (2 * p.granule) == 0) p.granule *= 2, ++p.granule_log2;
-    // floor(k / d) = floor(k m / 2^(31 + l)) for k < 2^31, with 2^(l - 1) < d <= 2^l and
-    // m = ceil(2^(31 + l) / d), which is at most 2^32 - 1
-    int l2 = 3;
-    while ((1ll << l2) < a.page_size) ++l2;
-    p.page_mul = static_cast<uint32_t>(((1ull << (31 + l2)) + a.page_size - 1) / a.page_size);
-    p.page_shift = l2 - 1;
+    p.page = divisor(a.page_size);
     if (a.T > 0 && (!encode_cache(&p.tk, p.kpos, a.k_cache, a, a.skc, d.D, f16, p.granule) ||
                     !encode_cache(&p.tv, p.vpos, a.v_cache, a, a.svc, d.D, f16, p.granule)))
         return cudaErrorInvalidValue;

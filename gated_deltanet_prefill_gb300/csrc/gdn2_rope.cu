@@ -102,7 +102,7 @@ __device__ __forceinline__ Place place_of(const RopeParams &p, int64_t t, int la
     r.place = p.kv_lens[n] - (end - t);
     if (t >= end || r.place < 0 || r.place >= static_cast<int64_t>(p.max_pages) * p.page_size) return r;
     const int at = static_cast<int>(r.place);
-    const int col = at / p.page_size;
+    const int col = quotient(at, p.page);
     r.slot = at - col * p.page_size;
     r.page = p.table[n * p.table_stride + col];
     r.ok = r.page >= 0 && r.page < p.num_pages;
@@ -133,8 +133,8 @@ __device__ void check_tables(const RopeParams &p) {
                 if (len < b - a || len > static_cast<int64_t>(p.max_pages) * p.page_size) {
                     bad_page = 1;
                 } else {
-                    col0 = static_cast<int>((len - (b - a)) / p.page_size);
-                    cols = static_cast<int>((len - 1) / p.page_size) + 1 - col0;
+                    col0 = quotient(static_cast<int>(len - (b - a)), p.page);
+                    cols = quotient(static_cast<int>(len) - 1, p.page) + 1 - col0;
                 }
             }
         }
@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks) gdn2_rope_kernel(cons
         return;
     }
     const int lane = threadIdx.x & 31, c = lane % L, sub = lane / L;
-    const int64_t warp = static_cast<int64_t>(blockIdx.x - (PAGED ? 1 : 0)) * kWarps + (threadIdx.x >> 5);
-    const int64_t t = warp / slices;
+    const uint32_t warp = (blockIdx.x - (PAGED ? 1 : 0)) * kWarps + (threadIdx.x >> 5);  // (T is below 2^31, or slices 1)
+    const int64_t t = slices == 1 ? warp : warp / slices;
     if (t >= p.T) return;
     const int r0 = static_cast<int>(warp - t * slices) * rows_per_slice;
     const int r1 = min(r0 + rows_per_slice, p.HQ + p.HK + p.HV);
