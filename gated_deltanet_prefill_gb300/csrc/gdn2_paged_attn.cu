@@ -14,8 +14,8 @@
 // kernel joins them in the order of the segments.  So one long sequence, many
 // short ones and any mixture fill the GPU alike, and the result does not depend on
 // timing.  Every CTA finds its own share from the lengths (a sum over the
-// sequences), which takes about a microsecond; a separate planning kernel cost 4 to
-// 25.
+// sequences), which takes about two microseconds; a separate planning kernel cost 4
+// to 25.
 //
 // A CTA (384 threads):
 //   warps 0-3, 4-7  two softmax groups, a thread per row
@@ -45,12 +45,12 @@
 //                   tensor pipe active 78 %.  Two row tiles of 128 keys take 2.55 k
 //                   cycles, their products 2.05 k, a softmax 1.5 k
 //   short chunks    the items' ends, when the tensor cores wait: 8 of 396 .. 3235 tokens,
-//                   16 heads, 246 to 258 us, 1.02 to 1.07 PFLOP/s
+//                   16 heads, pages of 16, 216 to 230 us, 1.15 to 1.22 PFLOP/s
 //   D = 64          the softmax's latency, 2.2 k cycles a tile: 16384 tokens, 16 heads,
-//                   546 us, 1.0 PFLOP/s
-//   decode          memory: 128 sequences of up to 8192 keys, 8 key heads of 128, 356 to
-//                   368 us, 6.5 to 6.7 TB/s of the 6.78 that a copy reaches
-//   one token       13 us: a chain of loads and of code that is fetched as it runs
+//                   549 us, 1.0 PFLOP/s
+//   decode          memory: 128 sequences of up to 8192 keys, 8 key heads of 128, 355 to
+//                   366 us, 6.5 to 6.7 TB/s of the 6.78 that a copy reaches
+//   one token       12 us: a chain of loads and of code that is fetched as it runs
 #include <cudaTypedefs.h>
 
 #include <type_traits>

@@ -14,8 +14,8 @@
 // interleaved one the partner is in the lane) and 16 multiply-adds.
 //
 // Bound by memory: 32768 tokens of 32 + 32 heads (half of each head rotated) take
-// 178 us, 6.03 TB/s of the 6.78 that a copy reaches; the append of 34997 tokens of
-// 32 + 32 + 32 heads to pages of 16 takes 263 us, 6.54 TB/s.  The packed fp32
+// 176 us, 6.10 TB/s of the 6.78 that a copy reaches; the append of 34997 tokens of
+// 32 + 32 + 32 heads to pages of 16 takes 264 us, 6.52 TB/s.  The packed fp32
 // instructions keep the issue slots below what the loads need.  A warp takes all
 // heads of a token when there are tokens enough to fill the GPU, and a slice of
 // them otherwise, so that a decode step is one row group per warp (128 tokens of
