@@ -70,6 +70,7 @@ struct AttnParams {
     int N, HQ, HKV, G;                  // G = HQ / HKV query heads per key head
     int page_size, max_pages;
     int causal, window;                 // window < 0: none
+    int lead;                           // of an item of two row tiles, in key tiles
     float scale;
     int *status;
 };

@@ -47,7 +47,7 @@
 //   short chunks    the items' ends, when the tensor cores wait: 8 of 396 .. 3235 tokens,
 //                   16 heads, pages of 16, 216 to 230 us, 1.15 to 1.22 PFLOP/s
 //   D = 64          the softmax's latency, 2.2 k cycles a tile: 16384 tokens, 16 heads,
-//                   549 us, 1.0 PFLOP/s
+//                   536 us, 1.03 PFLOP/s
 //   decode          memory: 128 sequences of up to 8192 keys, 8 key heads of 128, 355 to
 //                   366 us, 6.5 to 6.7 TB/s of the 6.78 that a copy reaches
 //   one token       12 us: a chain of loads and of code that is fetched as it runs
@@ -69,10 +69,12 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
 // What an item of two row tiles costs beside its key tiles, in key tiles: its
 // queries, its first softmax and its epilogue, when the tensor cores wait.
-// Measured on 8 chunks of 396 .. 3235 tokens (16 heads; 4 to 13 items per CTA): 286 us
-// without, 276 with 1, 267 with 2 and 3, 270 with 4, 276 with 6; 16384 tokens of
-// one sequence 734 -> 717.  An item of one row tile hides it behind its loads.
-constexpr int kLead = 2;
+// Measured with D = 128 on 8 chunks of 396 .. 3235 tokens (16 heads; 4 to 13 items per
+// CTA): 229 us with 1, 219 with 2, 221 with 3, 224 with 4 (and 286 without against 267 with
+// 2 before the loaders' divisions went); with D = 64 on 16384 tokens of one sequence (16
+// heads) 553 us without, 536 with 1, 548 with 2.  An item of one row tile hides it
+// behind its loads.
+constexpr int lead_tiles(int D) { return D == 128 ? 2 : 1; }
 constexpr int kSegRing = 8;     // segments in flight between the warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -145,14 +147,14 @@ __device__ __forceinline__ Span key_span(const AttnParams &a, int len, int fresh
 }
 // What an item costs beside its key tiles (the items have `tokens` new tokens but for
 // the last of a sequence; more than half of that makes two row tiles).
-__device__ __forceinline__ int lead_of(int fresh, int tokens, int m) {
-    return min(fresh - m * tokens, tokens) > tokens / 2 ? kLead : 0;
+__device__ __forceinline__ int lead_of(const AttnParams &a, int fresh, int tokens, int m) {
+    return min(fresh - m * tokens, tokens) > tokens / 2 ? a.lead : 0;
 }
 // What an item costs: its key tiles, at least 1 (an item without keys writes zeros),
 // after the lead.
 __device__ __forceinline__ int item_cost(const AttnParams &a, int len, int fresh, int tokens, int m) {
     const Span s = key_span(a, len, fresh, m * tokens, min(fresh, (m + 1) * tokens));
-    return max(1, s.hi - s.lo) + lead_of(fresh, tokens, m);
+    return max(1, s.hi - s.lo) + lead_of(a, fresh, tokens, m);
 }
 
 // sum over i < n of floor((a i + b) / 128); a n + b < 2^32.
@@ -187,7 +189,7 @@ __device__ __forceinline__ bool closed_form(const AttnParams &a, int len, int fr
 // The cost of a sequence's first `items` items.
 __device__ long long cost_of(const AttnParams &a, int len, int fresh, int tokens, int items) {
     if (items <= 0) return 0;
-    const long long lead = static_cast<long long>(items - 1) * kLead + lead_of(fresh, tokens, items - 1);
+    const long long lead = static_cast<long long>(items - 1) * a.lead + lead_of(a, fresh, tokens, items - 1);
     if (!a.causal) return lead + static_cast<long long>(items) * max(1, (len + kTile - 1) / kTile);
     // item m: ceil((len - fresh + min(fresh, (m + 1) tokens)) / 128); the last one apart
     const long long last = (len - fresh + min(static_cast<long long>(fresh), static_cast<long long>(items) * tokens) + kTile - 1) / kTile;
@@ -394,7 +396,7 @@ struct Walk {
         if (left <= 0) return false;
         const int j0 = m * tokens;
         const Span s = key_span(a, q.len, q.fresh, j0, min(q.fresh, j0 + tokens));
-        const int lead = lead_of(q.fresh, tokens, m), tiles = max(1, s.hi - s.lo), cost = lead + tiles;
+        const int lead = lead_of(a, q.fresh, tokens, m), tiles = max(1, s.hi - s.lo), cost = lead + tiles;
         const int take = static_cast<int>(min(static_cast<long long>(cost - off), left));
         const int from = max(0, off - lead), to = max(0, off + take - lead);  // key tiles
         left -= take;
@@ -1488,6 +1490,7 @@ cudaError_t launch_paged_attn(const AttnParams &a, const gdn2_attn_dims &d, int 
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.scale_log2 = a.scale * kLog2e;
+    p.a.lead = lead_tiles(d.D);
     p.ctas = ctas;
     p.tt = kTile / a.G;
     p.granule = 8;
