@@ -1350,7 +1350,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks) gdn2_attn_combin
         const int row = (task - (cta > 0 ? upto[cta - 1] : 0)) * RW + sub;
         // the row's token, if it has one, and head
         const int tile = row / kTile, in = row % kTile, tk = static_cast<int>((in * inv_g) >> 16), tok = tile * p.tt + tk;
-        if (tk >= p.tt || tok >= g.ntok) continue;  // (no collective operation follows in this round)
+        if (tk >= p.tt || tok >= g.ntok) continue;  // (no collective operation follows before the next task)
         float M = -INFINITY, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = 0; k0 <= g.more; k0 += kPieces) {
