@@ -78,6 +78,25 @@ constexpr int lead_tiles(int D) { return D == 128 ? 2 : 1; }
 constexpr int kSegRing = 8;     // segments in flight between the warps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// The softmax's weights are 2^(score - reference + bias) (scores times log2 e), rounded to
+// the call's type, since a product has one 16-bit type for both operands: a relative
+// error of up to 2^-8 (bf16) or 2^-11 (fp16) per weight, as the output has from its own
+// rounding, and less where they average out.  The reference is a maximum of the row's
+// keys so far, moved when a tile's maximum is more than kLag above it: the outputs are
+// then seldom rescaled.
+// bf16 has fp32's exponents and needs no bias.  fp16 ends at 2^16, holds 2^-14 in full
+// and has nothing below 2^-25: with the weights up to 2^(kLag + kBias) = 2^15, one that
+// is 2^-25 of its reference still is held in full.  Many small weights beside a few
+// large ones may be what the output consists of (a key that takes nearly all weight and
+// whose value is next to nothing), so in fp16 the reference also moves down to a tile that
+// stays kDrop below it: tiles of small weights are held to their own maximum.  The
+// sums then grow instead, in fp32, to at most kMost.  Looking for such tiles costs 4 % with
+// D = 64 (16384 tokens of 16 heads 538 -> 560 us; kLag 4, 6 and 8 alike), nothing with D = 128.
+template <bool F16>
+struct Weights {
+    static constexpr float kLag = F16 ? 4.f : 8.f, kBias = F16 ? 11.f : 0.f, kDrop = 12.f;
+    static constexpr float kMost = 7.9e28f;  // 2^96; times values to 2^16 and pieces to 2^8 within fp32
+};
 // Registers: three warpgroups of 168 at launch, 64512 in all; the two softmax
 // groups, which hold a row of scores, take 192 and the third keeps 120
 // (2 x 128 x 192 + 128 x 120 = 64512).
@@ -1000,7 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
         const int x = wp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(wp & 3) << 21;  // TMEM lane of the warp's first row
         const uint32_t inv_g = 65536u / a.G + 1;                     // r / G for r < 128
-        const float sl2 = p.scale_log2, slack = fminf(8.f / sl2, 1e38f);
+        using W = Weights<F16>;
+        const float sl2 = p.scale_log2, slack = fminf(W::kLag / sl2, 1e38f), drop = fminf(W::kDrop / sl2, 1e38f);
         const int my_tok = static_cast<int>((row * inv_g) >> 16), my_head = row - my_tok * a.G;
         // A group signals with one arrival per warp: 128 arrivals on one barrier
         // take their turns, which the products waited for.
@@ -1070,17 +1090,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
 #pragma unroll
                     for (int c = 0; c < 128; c += 2)
                         mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], u[c >> 5][c & 31], u[c >> 5][(c & 31) + 1]);
-                    const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if (i == begin) {
                         m = top;
                     } else {
-                        // The maximum in use may lag behind the true one by a
-                        // factor of 2^8 (weights to 256 lose nothing in 16-bit
-                        // floating point): the outputs are then seldom rescaled.
-                        const bool grow = top > m + slack;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float f = grow ? ex2((m - top) * sl2) : 1.f;
-                            if (grow) m = top;
+                        const bool grow = top > m + slack, fall = F16 && top < m - drop && top > -INFINITY;
+                        if (__any_sync(0xffffffffu, grow || fall)) {
+                            float f = 1.f;
+                            if (grow || fall) {
+                                f = ex2((m - top) * sl2);
+                                if (!fall || l * f < W::kMost) m = top;
+                                else f = 1.f;
+                            }
                             l *= f;
                             used();
 #pragma unroll 1
@@ -1094,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                             }
                         }
                     }
-                    const float base = m == -INFINITY ? 0.f : m * sl2;
+                    const float base = m == -INFINITY ? 0.f : m * sl2 - W::kBias;
                     const uint64_t scale2 = pair(sl2, sl2), base2 = pair(-base, -base);
                     uint64_t sum2[4] = {0, 0, 0, 0};
                     // The weights in groups of 8 scores, three of them under way: the
@@ -1176,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn2_paged_attn_kernel(const __gr
                     l = f0 * l + f1 * ml.y;
                 }
                 if (tok >= 0) {
-                    const float base = m == -INFINITY ? -INFINITY : m * sl2;
+                    const float base = m == -INFINITY ? -INFINITY : m * sl2 - W::kBias;
                     if (!whole)
                         p.part_ml[part] = make_float2(base, l);
                     else if (a.lse)
