@@ -134,8 +134,8 @@ void fill_rope(RopeParams &p, const gdn2_attn_dims &d, const void *q, const void
     memset(&p, 0, sizeof(p));
     p.q = static_cast<const bf16 *>(q);
     p.k = static_cast<const bf16 *>(k);
-    p.q_weight = static_cast<const bf16 *>(q_weight);
-    p.k_weight = static_cast<const bf16 *>(k_weight);
+    p.q_weight = d.norm ? static_cast<const bf16 *>(q_weight) : nullptr;  // the weights are part of the norm
+    p.k_weight = d.norm ? static_cast<const bf16 *>(k_weight) : nullptr;
     p.inv_freq = inv_freq;
     p.positions = positions;
     p.pos64 = d.positions_i64 ? 1 : 0;

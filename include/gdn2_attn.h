@@ -97,7 +97,7 @@ GDN2_API gdn2_status gdn2_attn_dims_init(gdn2_attn_dims *dims, int64_t T_tot, in
  *
  *   q, q_out            both NULL: queries are left out; likewise k, k_out
  *                       (not both pairs)
- *   q_weight, k_weight  may be NULL: weight 1
+ *   q_weight, k_weight  may be NULL: weight 1; not used with norm = 0
  *   inv_freq, positions may be NULL when rot_dim = 0
  *   q_out, k_out        may be q, k themselves (same strides): in place; any
  *                       other overlap with an input is GDN2_ERR_ALIAS

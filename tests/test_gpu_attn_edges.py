@@ -7,7 +7,7 @@ import torch
 
 from attn_reference import UNIT, attention, f64
 from gated_deltanet_prefill_gb300 import attn
-from test_gpu_attn import BF, FP, Cache, gen, normal
+from test_gpu_attn import BF, FP, Cache, gen, ints, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,29 @@ def test_attention_beside_keys_far_above_the_rest(cuda_lib, new, past, page, HQ,
     worst = (np.abs(f64(out) - ref) / tol).max()
     assert worst <= 1.0, worst
     assert (np.abs(f64(lse) - z) <= scores).all()
+
+
+def test_weights_without_the_norm_are_not_used(cuda_lib):
+    """The weights belong to the norm: a C caller that passes them with norm = 0 gets the rows without either."""
+    g = gen(51)
+    lib = attn.load()
+    T, HQ, HK, D, page = 9, 3, 2, 64, 16
+    q, k, v = normal(g, T, HQ, D), normal(g, T, HK, D), normal(g, T, HK, D)
+    w = 2 + normal(g, D).abs()
+    f, _ = attn.rope_frequencies(D)
+    pos = ints(list(range(T)))
+    want_q, want_k = attn.qk_norm_rope(q, k, pos, f, norm=False)
+    c = Cache(g, [T], [0], page, HK, D)
+    dims = attn.AttnDims()
+    assert lib.gdn2_attn_dims_init(dims, T, 1, HQ, HK, D, c.k.shape[0], page, c.table.shape[1]) == 0
+    dims.norm = 0
+    qo, ko, ws = torch.zeros_like(q), torch.zeros_like(k), torch.zeros(64, dtype=torch.uint8, device="cuda")
+    p = [x.data_ptr() for x in (q, k, w, w, f, pos, qo, ko)]
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.gdn2_qk_norm_rope(*p, dims, stream) == 0
+    assert torch.equal(qo, want_q) and torch.equal(ko, want_k)
+    qo.zero_()
+    p = [x.data_ptr() for x in (q, k, v, w, w, f, pos, c.cu, c.lens, c.table, qo, c.k, c.v)]
+    assert lib.gdn2_kv_append(*p, dims, ws.data_ptr(), 64, stream) == 0
+    rows = c.k[int(c.table[0, 0]), :T]
+    assert attn.device_status(ws) == 0 and torch.equal(qo, want_q) and torch.equal(rows, want_k)
