@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(32 * kWarps, kMinBlocks) gdn2_rope_kernel(cons
             for (int e = 0; e < 4; ++e) {
                 A[e] = INTER ? pair(wa[2 * e] * cs[e], wa[2 * e + 1] * cs[e]) : pair(wa[2 * e] * cs[INTER ? 0 : 2 * e], wa[2 * e + 1] * cs[INTER ? 0 : 2 * e + 1]);
                 B[e] = INTER ? pair(wb[2 * e + 1] * -sn[e], wb[2 * e] * sn[e]) : pair(wb[2 * e] * sn[INTER ? 0 : 2 * e], wb[2 * e + 1] * sn[INTER ? 0 : 2 * e + 1]);
+                if (!turned) B[e] = 0;  // (0 x inf is NaN)
             }
         }
         const int src = lane - c + partner;

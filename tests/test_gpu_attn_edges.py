@@ -92,3 +92,22 @@ def test_weights_without_the_norm_are_not_used(cuda_lib):
     assert lib.gdn2_kv_append(*p, dims, ws.data_ptr(), 64, stream) == 0
     rows = c.k[int(c.table[0, 0]), :T]
     assert attn.device_status(ws) == 0 and torch.equal(qo, want_q) and torch.equal(rows, want_k)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinite_weight_of_a_channel_that_does_not_turn(cuda_lib, inter, D):
+    """y = x w / rms(x) there: infinite in that channel, and of no effect on any other."""
+    g = gen(52)
+    q = normal(g, 5, 3, D)
+    assert (q != 0).all()
+    w = 1 + normal(g, D) / 4
+    f, _ = attn.rope_frequencies(32)
+    pos = ints([0, 1, 2, 77, 4095])
+    want, _ = attn.qk_norm_rope(q, None, pos, f, interleaved=inter, q_weight=w)
+    at = [32, 45, D - 1]
+    w[at] = float("inf")
+    y, _ = attn.qk_norm_rope(q, None, pos, f, interleaved=inter, q_weight=w)
+    assert torch.equal(y[..., at], torch.sign(q[..., at]) * float("inf"))
+    rest = [i for i in range(D) if i not in at]
+    assert torch.equal(y[..., rest], want[..., rest])
