@@ -178,9 +178,11 @@ def _check_paged(k_cache, v_cache, table, lens, cu):
     size, stride, dtype, cuda = table
     if not cuda or dtype != torch.int32 or len(size) != 2 or size[0] != n or (size[1] > 1 and stride[1] != 1):
         raise ValueError("block_table must be an int32 CUDA tensor [sequences, pages] with contiguous rows")
+    if n > 1 and stride[0] < size[1]:
+        raise ValueError("block_table: the rows lie on top of one another (one row expanded to all sequences?)")
     _check_flat("cu_seqlens", cu, (torch.int32, torch.int64))
     _check_flat("kv_lens", lens, (torch.int32,), n)
-    return n, kc[:3], vc[:3], max(stride[0], size[1]), size[1], 1 if cu[1] == torch.int64 else 0
+    return n, kc[:3], vc[:3], stride[0] if n > 1 else size[1], size[1], 1 if cu[1] == torch.int64 else 0
 
 
 def _norm_rope_dims(q, k, q_out, k_out, q_weight, k_weight, inv_freq, positions, norm, interleaved, eps, rope_factor):
@@ -263,7 +265,7 @@ def append_kv(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q=None, 
 
     k, v [T, HKV, D]; k_cache, v_cache [pages, page_size, HKV, D] (any strides;
     pass a transposed view for head-major pages); block_table [N, max_pages]
-    int32; cu_seqlens [N + 1] int32/int64; kv_lens [N] int32, the cached tokens
+    int32, its rows apart; cu_seqlens [N + 1] int32/int64; kv_lens [N] int32, the cached tokens
     of each sequence with the new ones.  The rotation's positions are the
     tokens' places in the cached sequences unless given.  ``device_status`` on
     the workspace reports a bad length, place or table entry.  Returns q_out

@@ -40,7 +40,8 @@ extern "C" {
  *                    the page, head): token-major and head-major pages are
  *                    both views of this shape
  *   block_table      [N, max_pages]    int32; entry j of row n is the page of
- *                    tokens j * page_size .. of sequence n
+ *                    tokens j * page_size .. of sequence n; table_stride is at
+ *                    least max_pages
  *   cu_seqlens       [N + 1]           int32, or int64 with cu_seqlens_i64 = 1:
  *                    the new tokens of sequence n are rows cu[n] .. cu[n + 1)
  *   kv_lens          [N]               int32: tokens of sequence n in the cache
