@@ -265,11 +265,11 @@ def append_kv(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, q=None, 
 
     k, v [T, HKV, D]; k_cache, v_cache [pages, page_size, HKV, D] (any strides;
     pass a transposed view for head-major pages); block_table [N, max_pages]
-    int32, its rows apart; cu_seqlens [N + 1] int32/int64; kv_lens [N] int32, the cached tokens
-    of each sequence with the new ones.  The rotation's positions are the
+    int32, its rows apart; cu_seqlens [N + 1] int32/int64; kv_lens [N] int32, the
+    cached tokens of each sequence with the new ones.  The rotation's positions are the
     tokens' places in the cached sequences unless given.  ``device_status`` on
-    the workspace reports a bad length, place or table entry.  Returns q_out
-    (None without q).
+    the workspace (contiguous, on the inputs' device) reports a bad length,
+    place or table entry.  Returns q_out (None without q).
     """
     if _call is None:
         load()

@@ -115,6 +115,14 @@ struct Args {
     }
 };
 
+// Whether a workspace that the caller passed is plain memory on the device of `like`
+// (the library gets its address and its bytes); sets an exception if not.
+bool workspace_ok(const Args &args, const at::Tensor *workspace, const at::Tensor *like) {
+    if (!args.ok || !workspace || (workspace->device() == like->device() && workspace->is_contiguous())) return true;
+    PyErr_SetString(PyExc_ValueError, "workspace must be contiguous, on the device of the inputs");
+    return false;
+}
+
 // The plan of the call: the known one, or the one that `dims` (bytes of the struct)
 // brings.  Returns false where there is none, with or without an exception set.
 bool find(Plans &plans, const Key &key, Args &args, Plan &plan) {
@@ -242,6 +250,7 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *q_out = args.tensor(), *workspace = args.tensor();
     PyObject *stream = args.next();
     if (!k || !v || !k_cache || !v_cache || !table || !lens || !cu) args.ok = false;
+    if (!workspace_ok(args, workspace, k)) return nullptr;
     for (const at::Tensor *t : {k, v, k_cache, v_cache, table, q, q_out}) key.rows(t);
     for (const at::Tensor *t : {lens, cu, positions, inv_freq, q_weight, k_weight}) key.flat(t);
     Plan plan;
@@ -287,6 +296,7 @@ PyObject *paged_attn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *workspace = args.tensor();
     PyObject *stream = args.next();
     if (!q || !k_cache || !v_cache || !table || !lens || !cu) args.ok = false;
+    if (!workspace_ok(args, workspace, q)) return nullptr;
     for (const at::Tensor *t : {q, k_cache, v_cache, table, out}) key.rows(t);
     for (const at::Tensor *t : {lens, cu, lse}) key.flat(t);
     Plan plan;

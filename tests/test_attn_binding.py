@@ -33,3 +33,47 @@ def test_block_table_rows_on_top_of_one_another_are_refused(shape, stride):
     table = torch.zeros(100, dtype=torch.int32).as_strided(shape, stride)
     with pytest.raises(ValueError, match="block_table"):
         paged_metadata(table)
+
+
+def calls(x, workspace):
+    """append_kv and paged_attn_fwd on tensors like x, with the workspace."""
+    i32 = torch.zeros(4, dtype=torch.int32, device=x.device)
+    cache = torch.zeros(3, 16, 2, 64, dtype=x.dtype, device=x.device)
+    other = torch.zeros_like(cache)
+    yield lambda: attn.append_kv(x, x, cache, other, i32[None], i32[:1], i32[:2], workspace=workspace)
+    yield lambda: attn.paged_attn_fwd(x, cache, other, i32[None], i32[:1], i32[:2], workspace=workspace)
+
+
+def refused_workspaces(device):
+    """A workspace elsewhere (the meta device stands in for the CPU beside a GPU), and one whose bytes do not lie together:
+    its size in bytes passes the library's check, its memory is not its own."""
+    yield torch.empty(1 << 26, dtype=torch.uint8, device="meta" if device == "cpu" else "cpu")
+    yield torch.empty(1 << 12, dtype=torch.uint8, device=device)[::2]
+    yield torch.empty(1, dtype=torch.uint8, device=device).expand(1 << 26)
+    yield torch.empty(64, 64, dtype=torch.float32, device=device).t()
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from gated_deltanet_prefill_gb300 import build
+    build.build()
+    return attn.load()
+
+
+def test_workspaces_that_are_not_plain_memory_beside_the_inputs_are_refused(lib):
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    for workspace in refused_workspaces("cpu"):
+        for call in calls(x, workspace):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
+
+
+@pytest.mark.gpu
+def test_workspaces_refused_on_the_gpu(cuda_lib):
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for call in calls(x, torch.empty(1 << 26, dtype=torch.uint8, device="cuda")):
+        call()  # known metadata from here on
+    for workspace in refused_workspaces("cuda"):
+        for call in calls(x, workspace):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
