@@ -16,6 +16,7 @@
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -123,6 +124,19 @@ bool workspace_ok(const Args &args, const at::Tensor *workspace, const at::Tenso
     return false;
 }
 
+// Whether a call's tensors are all on one device; sets an exception if not.
+bool one_device(const Args &args, std::initializer_list<const at::Tensor *> tensors) {
+    const at::Tensor *first = nullptr;
+    for (const at::Tensor *t : tensors) {
+        if (!args.ok || !t) continue;
+        if (!first) first = t;
+        if (t->device() == first->device()) continue;
+        PyErr_SetString(PyExc_ValueError, "the tensors of a call must be on one device");
+        return false;
+    }
+    return true;
+}
+
 // The plan of the call: the known one, or the one that `dims` (bytes of the struct)
 // brings.  Returns false where there is none, with or without an exception set.
 bool find(Plans &plans, const Key &key, Args &args, Plan &plan) {
@@ -161,7 +175,8 @@ at::Tensor empty(at::IntArrayRef size, at::ScalarType dtype, const at::Tensor &l
     return at::Tensor(at::detail::empty_cuda(size, dtype, like.device(), std::nullopt));
 }
 // Where the call runs: the stream given (an address), or the current one of the
-// tensor's device.
+// tensor's device.  The calls make that device the current one first (CUDAGuard): the
+// library launches on the current device, whatever its pointers are.
 struct Stream {
     void *handle = nullptr;
     bool other = false;  // not the current one
@@ -209,11 +224,13 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *q_out = args.tensor(), *k_out = args.tensor();
     PyObject *stream = args.next();
     if (!q) args.ok = false;
+    if (!one_device(args, {q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out})) return nullptr;
     for (const at::Tensor *t : {q, k, q_out, k_out}) key.rows(t);
     for (const at::Tensor *t : {positions, inv_freq, q_weight, k_weight}) key.flat(t);
     Plan plan;
     if (!find(plans, key, args, plan)) return unknown();
     const gdn2_attn_dims &d = plan.dims;
+    const c10::cuda::CUDAGuard guard(q->device());
     const Stream s(stream, *q);
     if (PyErr_Occurred()) return nullptr;
     at::Tensor qo, ko;
@@ -250,12 +267,15 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *q_out = args.tensor(), *workspace = args.tensor();
     PyObject *stream = args.next();
     if (!k || !v || !k_cache || !v_cache || !table || !lens || !cu) args.ok = false;
-    if (!workspace_ok(args, workspace, k)) return nullptr;
+    if (!workspace_ok(args, workspace, k) ||
+        !one_device(args, {k, v, k_cache, v_cache, table, lens, cu, q, positions, inv_freq, q_weight, k_weight, q_out}))
+        return nullptr;
     for (const at::Tensor *t : {k, v, k_cache, v_cache, table, q, q_out}) key.rows(t);
     for (const at::Tensor *t : {lens, cu, positions, inv_freq, q_weight, k_weight}) key.flat(t);
     Plan plan;
     if (!find(plans, key, args, plan)) return unknown();
     const gdn2_attn_dims &d = plan.dims;
+    const c10::cuda::CUDAGuard guard(k->device());
     const Stream s(stream, *k);
     if (PyErr_Occurred()) return nullptr;
     at::Tensor qo, ws;
@@ -296,12 +316,13 @@ PyObject *paged_attn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *workspace = args.tensor();
     PyObject *stream = args.next();
     if (!q || !k_cache || !v_cache || !table || !lens || !cu) args.ok = false;
-    if (!workspace_ok(args, workspace, q)) return nullptr;
+    if (!workspace_ok(args, workspace, q) || !one_device(args, {q, k_cache, v_cache, table, lens, cu, out, lse})) return nullptr;
     for (const at::Tensor *t : {q, k_cache, v_cache, table, out}) key.rows(t);
     for (const at::Tensor *t : {lens, cu, lse}) key.flat(t);
     Plan plan;
     if (!find(plans, key, args, plan)) return unknown();
     const gdn2_attn_dims &d = plan.dims;
+    const c10::cuda::CUDAGuard guard(q->device());
     const Stream s(stream, *q);
     if (PyErr_Occurred()) return nullptr;
     at::Tensor o, l, ws;

@@ -77,3 +77,36 @@ def test_workspaces_refused_on_the_gpu(cuda_lib):
         for call in calls(x, workspace):
             with pytest.raises(ValueError, match="workspace"):
                 call()
+
+
+def arguments(device):
+    """The tensor arguments of the three calls, by call."""
+    def zeros(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    rows = zeros(4, 2, 64)
+    rotary = dict(positions=zeros(4, dtype=torch.int32), inv_freq=zeros(32, dtype=torch.float64), q_weight=zeros(64),
+                  k_weight=zeros(64), q_out=zeros(4, 2, 64))
+    cache = dict(k_cache=zeros(3, 16, 2, 64), v_cache=zeros(3, 16, 2, 64), block_table=zeros(1, 3, dtype=torch.int32),
+                 kv_lens=zeros(1, dtype=torch.int32), cu_seqlens=zeros(2, dtype=torch.int32))
+    return {attn.qk_norm_rope: dict(q=rows, k=rows, k_out=zeros(4, 2, 64), **rotary),
+            attn.append_kv: dict(k=rows, v=rows, q=rows, **cache, **rotary),
+            attn.paged_attn_fwd: dict(q=rows, **cache, out=zeros(4, 2, 64), lse=zeros(4, 2, dtype=torch.float32))}
+
+
+def test_tensors_of_two_devices_are_refused(lib):
+    """One argument after the other on another device than the rest (the meta device stands in for a second GPU)."""
+    for call, args in arguments("cpu").items():
+        for name in args:
+            with pytest.raises(ValueError, match="one device"):
+                call(**{**args, name: args[name].to("meta")})
+
+
+@pytest.mark.gpu
+def test_tensors_of_two_devices_are_refused_on_the_gpu(cuda_lib):
+    args = arguments("cuda")
+    for call in args:
+        call(**args[call])  # known metadata from here on
+        for name in args[call]:
+            with pytest.raises(ValueError, match="one device"):
+                call(**{**args[call], name: args[call][name].cpu()})
