@@ -178,15 +178,18 @@ def state_heads(q, v) -> int:
     return max(q.shape[1], v.shape[1])
 
 
-def _check_inputs(q, k, v, cu_seqlens, initial_state):
+def _check_inputs(q, k, v, cu_seqlens, initial_state, **others):
     """The checks every wrapper makes before marshalling: packed input with
-    cu_seqlens, CUDA tensors, and a contiguous initial state (the C ABI takes
-    the state without strides)."""
+    cu_seqlens, CUDA tensors of one device, and a contiguous initial state (the
+    C ABI takes the state without strides)."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required (packed input only)")
-    for name, t in (("q", q), ("k", k), ("v", v), ("cu_seqlens", cu_seqlens), ("initial_state", initial_state)):
+    for name, t in (("q", q), ("k", k), ("v", v), ("cu_seqlens", cu_seqlens), ("initial_state", initial_state),
+                    *others.items()):
         if t is not None and not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % name)
+        if t is not None and t.device != q.device:
+            raise ValueError("%s must be on q's device" % name)
     if initial_state is not None and not initial_state.is_contiguous():
         raise ValueError("initial_state must be contiguous [N, HS, K, V]")
 
@@ -205,7 +208,8 @@ def chunk_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_state
     [N, HS, K, V] or None).
     """
     lib = load()
-    _check_inputs(q, k, v, cu_seqlens, initial_state)
+    _check_inputs(q, k, v, cu_seqlens, initial_state, g=g, beta=beta, w=w, out=out, final_state=final_state,
+                  workspace=workspace)
     T, H, K = q.shape
     V = v.shape[2]
     HS = state_heads(q, v)
@@ -226,11 +230,12 @@ def chunk_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_state
             ctypes.c_float(0.0 if scale is None else float(scale)),
             _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
             ctypes.byref(dims), _ptr(workspace), workspace.numel(), stream)
-    if stage_events is None:
-        st = lib.gdn2_chunk_fwd(*args)
-    else:
-        arr = (ctypes.c_void_p * len(stage_events))(*[e.cuda_event for e in stage_events])
-        st = lib.gdn2_chunk_fwd_staged(*args, arr, len(stage_events))
+    with torch.cuda.device(q.device):  # the library launches on the current device
+        if stage_events is None:
+            st = lib.gdn2_chunk_fwd(*args)
+        else:
+            arr = (ctypes.c_void_p * len(stage_events))(*[e.cuda_event for e in stage_events])
+            st = lib.gdn2_chunk_fwd_staged(*args, arr, len(stage_events))
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_chunk_fwd")
     return out, final_state
@@ -245,7 +250,7 @@ def chunk_gdn2_fwd_noalloc(q, k, v, g=None, beta=None, w=None, scale=None, initi
     the caller does not pass them; ``noalloc_device_status()`` reads the
     device-side status of the last call."""
     lib = load()
-    _check_inputs(q, k, v, cu_seqlens, initial_state)
+    _check_inputs(q, k, v, cu_seqlens, initial_state, g=g, beta=beta, w=w, out=out, final_state=final_state)
     T, H, K = q.shape
     V = v.shape[2]
     HS = state_heads(q, v)
@@ -258,10 +263,11 @@ def chunk_gdn2_fwd_noalloc(q, k, v, g=None, beta=None, w=None, scale=None, initi
     dims = make_dims(q, k, v, g, beta, w, out, cu_seqlens, use_qk_l2norm, impl, state_v_major, sdt)
     if stream is None:
         stream = torch.cuda.current_stream(q.device).cuda_stream
-    st = lib.gdn2_chunk_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(w),
-                                    ctypes.c_float(0.0 if scale is None else float(scale)),
-                                    _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
-                                    ctypes.byref(dims), stream)
+    with torch.cuda.device(q.device):
+        st = lib.gdn2_chunk_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(w),
+                                        ctypes.c_float(0.0 if scale is None else float(scale)),
+                                        _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
+                                        ctypes.byref(dims), stream)
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_chunk_fwd_noalloc")
     return out, final_state
@@ -275,7 +281,8 @@ def recurrent_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_s
     as ``chunk_gdn2_fwd``; ``final_state`` may be ``initial_state`` itself
     (updated in place).  Returns (out, final_state)."""
     lib = load()
-    _check_inputs(q, k, v, cu_seqlens, initial_state)
+    _check_inputs(q, k, v, cu_seqlens, initial_state, g=g, beta=beta, w=w, out=out, final_state=final_state,
+                  workspace=workspace)
     T, H, K = q.shape
     V = v.shape[2]
     HS = state_heads(q, v)
@@ -290,22 +297,24 @@ def recurrent_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_s
         workspace = torch.empty(256, dtype=torch.uint8, device=q.device)
     if stream is None:
         stream = torch.cuda.current_stream(q.device).cuda_stream
-    st = lib.gdn2_recurrent_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(w),
-                                ctypes.c_float(0.0 if scale is None else float(scale)),
-                                _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
-                                ctypes.byref(dims), _ptr(workspace), workspace.numel(), stream)
+    with torch.cuda.device(q.device):
+        st = lib.gdn2_recurrent_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(w),
+                                    ctypes.c_float(0.0 if scale is None else float(scale)),
+                                    _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
+                                    ctypes.byref(dims), _ptr(workspace), workspace.numel(), stream)
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_recurrent_fwd")
     return out, final_state
 
 
 def noalloc_device_status(device=None, stream=None) -> int:
-    """Device-side status of the last ``chunk_gdn2_fwd_noalloc`` call on the
-    current device (syncs the stream)."""
+    """Device-side status of the last ``chunk_gdn2_fwd_noalloc`` call on
+    ``device``, the current one by default (syncs the stream)."""
     if stream is None:
         stream = torch.cuda.current_stream(device).cuda_stream
     s = ctypes.c_int32(-1)
-    st = load().gdn2_noalloc_device_status(stream, ctypes.byref(s))
+    with torch.cuda.device(device):
+        st = load().gdn2_noalloc_device_status(stream, ctypes.byref(s))
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_noalloc_device_status")
     return int(s.value)
@@ -316,7 +325,8 @@ def device_status(workspace, stream=None) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(workspace.device).cuda_stream
     s = ctypes.c_int32(-1)
-    st = load().gdn2_device_status(_ptr(workspace), stream, ctypes.byref(s))
+    with torch.cuda.device(workspace.device):
+        st = load().gdn2_device_status(_ptr(workspace), stream, ctypes.byref(s))
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_device_status")
     return int(s.value)

@@ -1,10 +1,10 @@
-"""What the binding of the attention-layer operators refuses before any kernel
-could see it.  Host only: tensors on the CPU, or metadata alone.
+"""What the bindings refuse before any kernel could see it.  Host only, but for
+the tests marked gpu: tensors on the CPU, or metadata alone.
 """
 import pytest
 import torch
 
-from gated_deltanet_prefill_gb300 import attn
+from gated_deltanet_prefill_gb300 import attn, gdn2
 
 
 def paged_metadata(table):
@@ -110,3 +110,25 @@ def test_tensors_of_two_devices_are_refused_on_the_gpu(cuda_lib):
         for name in args[call]:
             with pytest.raises(ValueError, match="one device"):
                 call(**{**args[call], name: args[call][name].cpu()})
+
+
+class Tensor:
+    """What the GDN-2 binding's checks look at, on a device that this machine need not have."""
+    is_cuda, dtype, shape = True, torch.bfloat16, (4, 2, 64)
+
+    def __init__(self, index=0, device="cuda"):
+        self.device = torch.device(device, index)
+        self.is_cuda = device == "cuda"
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.mark.parametrize("call,more", [(gdn2.chunk_gdn2_fwd, ("workspace",)), (gdn2.recurrent_gdn2_fwd, ("workspace",)),
+                                       (gdn2.chunk_gdn2_fwd_noalloc, ())])
+def test_gdn2_calls_refuse_tensors_of_two_devices(lib, call, more):
+    names = ("q", "k", "v", "g", "beta", "w", "initial_state", "cu_seqlens", "out", "final_state") + more
+    for name in names[1:]:
+        for other in (Tensor(1), Tensor(0, "cpu")):
+            with pytest.raises(ValueError, match="q's device|must be a CUDA tensor"):
+                call(**{n: other if n == name else Tensor() for n in names})
