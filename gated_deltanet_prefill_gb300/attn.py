@@ -308,8 +308,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale=
     q [T, HQ, D] (HQ a multiple of the cache's heads); cache and tables as in
     ``append_kv``.  With ``causal`` a token attends to the keys up to its own
     place, with ``window_left`` >= 0 to at most that many before it (pages wholly
-    before the first new token's window are not read); scale None means
-    1/sqrt(D).  Returns out [T, HQ, D], or (out, lse [T, HQ] fp32) with
+    before the first new token's window are not read); scale is positive, None
+    means 1/sqrt(D).  Returns out [T, HQ, D], or (out, lse [T, HQ] fp32) with
     ``return_lse``; a token with no key gets zeros and lse -inf.
     """
     if _call is None:

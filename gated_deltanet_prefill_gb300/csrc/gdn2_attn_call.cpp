@@ -306,9 +306,16 @@ PyObject *paged_attn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Key key;
     const at::Tensor *q = args.tensor(), *k_cache = args.tensor(), *v_cache = args.tensor(), *table = args.tensor(),
                      *lens = args.tensor(), *cu = args.tensor();
-    double scale = 0.0;
-    if (args.a[args.i] == Py_None) ++args.i;
-    else scale = args.number();
+    float scale = 0.f;  // to the library: 1/sqrt(D)
+    if (args.a[args.i] == Py_None) {
+        ++args.i;
+    } else {
+        scale = static_cast<float>(args.number());
+        if (args.ok && !(scale > 0.f)) {
+            PyErr_SetString(PyExc_ValueError, "scale must be positive (None means 1/sqrt(D))");
+            return nullptr;
+        }
+    }
     key.add(static_cast<int64_t>(args.flag()));
     key.add(args.integer());
     const at::Tensor *out = args.tensor(), *lse = args.tensor();
@@ -334,7 +341,7 @@ PyObject *paged_attn_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     gdn2_status st;
     Py_BEGIN_ALLOW_THREADS
     st = paged_attn_fn(p[0], p[1], p[2], p[3], static_cast<const int32_t *>(p[4]), static_cast<const int32_t *>(p[5]),
-                       static_cast<float>(scale), p[6], static_cast<float *>(p[7]), &d, p[8], bytes, s.handle);
+                       scale, p[6], static_cast<float *>(p[7]), &d, p[8], bytes, s.handle);
     Py_END_ALLOW_THREADS
     s.keep({&o, &l, &ws});
     if (st != GDN2_OK) return failed(st, "gdn2_paged_attn_fwd");

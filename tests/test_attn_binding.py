@@ -132,3 +132,23 @@ def test_gdn2_calls_refuse_tensors_of_two_devices(lib, call, more):
         for other in (Tensor(1), Tensor(0, "cpu")):
             with pytest.raises(ValueError, match="q's device|must be a CUDA tensor"):
                 call(**{n: other if n == name else Tensor() for n in names})
+
+
+@pytest.mark.parametrize("scale", [0.0, 0, -0.125, -1, 1e-50, float("nan")])
+def test_scales_that_are_not_positive_are_refused(lib, scale):
+    """Not taken for "no scale given", which is 1/sqrt(D)."""
+    args = arguments("cpu")[attn.paged_attn_fwd]
+    with pytest.raises(ValueError, match="scale"):
+        attn.paged_attn_fwd(**args, scale=scale)
+
+
+@pytest.mark.gpu
+def test_scales_refused_on_the_gpu(cuda_lib):
+    args = arguments("cuda")[attn.paged_attn_fwd]
+    attn.paged_attn_fwd(**args, scale=0.25)  # known metadata from here on
+    for scale in (0.0, -0.125, 1e-50, float("nan")):
+        with pytest.raises(ValueError, match="scale"):
+            attn.paged_attn_fwd(**args, scale=scale)
+    with pytest.raises(gdn2.Gdn2Error) as e:
+        attn.paged_attn_fwd(**args, scale=float("inf"))
+    assert e.value.status == 2
