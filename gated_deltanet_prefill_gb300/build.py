@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into
 ``gated_deltanet_prefill_gb300/_build/libgdn2.so``.  The build is skipped when
 the library is newer than every source and header.  ``csrc/gdn2_attn_call.cpp``
 (a CPython module that calls the library for ``attn.py``) is compiled beside
-them with the host compiler.
+them with the host compiler; where that fails, the library is linked all the
+same, for the C ABI and ``gdn2.py``, before the error is raised.
 """
 from __future__ import annotations
 
@@ -107,8 +108,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         module = ex.submit(_build_call) if call else None
         list(ex.map(compile_one, zip(srcs, objs)))
-        if module:
-            module.result()
     tmp = lib + ".%d.tmp" % os.getpid()
     cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -116,6 +115,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
         print(" ".join(cmd)); print(r.stdout + r.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, lib)
+    if module:
+        module.result()  # (the library is there whether or not the module could be built)
     return lib
 
 
