@@ -68,9 +68,10 @@ def load():
         lib.gdn2_paged_attn_workspace_bytes.restype = _sz
         lib.gdn2_paged_attn_fwd.argtypes = [_vp] * 6 + [_f32, _vp, _vp, dims, _vp, _sz, _vp]
         lib.gdn2_paged_attn_fwd.restype = ctypes.c_int
-        if not os.path.exists(build.CALL):
-            raise RuntimeError("%s is not built; run __graft_entry__.build()" % os.path.basename(build.CALL))
-        spec = importlib.util.spec_from_file_location("gdn2_attn_call", build.CALL)
+        path = build.call_path()
+        if not os.path.exists(path):
+            raise RuntimeError("%s is not built; run __graft_entry__.build()" % os.path.basename(path))
+        spec = importlib.util.spec_from_file_location("gdn2_attn_call", path)
         call = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(call)
         call.bind(*(ctypes.cast(f, _vp).value for f in (lib.gdn2_qk_norm_rope, lib.gdn2_kv_append,

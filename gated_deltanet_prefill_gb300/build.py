@@ -25,7 +25,6 @@ LIB = os.path.join(BUILD, "libgdn2.so")
 # the checked build: the same sources with the device-side index checks on
 # (-DGDN2_CHECK_BOUNDS); built on request only (tests), never the product path
 LIB_CHECKED = os.path.join(BUILD, "libgdn2_checked.so")
-CALL = os.path.join(BUILD, "gdn2_attn_call.so")
 CALL_SOURCE = os.path.join(CSRC, "gdn2_attn_call.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -51,10 +50,17 @@ def _stale(lib=LIB) -> bool:
     return any(os.path.getmtime(f) > t for f in deps)
 
 
+def call_path() -> str:
+    """The calls module for this Python and this torch, whose internals it is compiled against."""
+    import torch
+    return os.path.join(BUILD, "gdn2_attn_call.%s-torch%s.so" % (sysconfig.get_config_var("SOABI"), torch.__version__))
+
+
 def _call_stale() -> bool:
-    if not os.path.exists(CALL):
+    call = call_path()
+    if not os.path.exists(call):
         return True
-    t = os.path.getmtime(CALL)
+    t = os.path.getmtime(call)
     return any(os.path.getmtime(f) > t for f in [CALL_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
@@ -64,7 +70,8 @@ def _build_call() -> None:
     lib = os.path.join(home, "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     os.makedirs(BUILD, exist_ok=True)
-    tmp = CALL + ".%d.tmp" % os.getpid()
+    call = call_path()
+    tmp = call + ".%d.tmp" % os.getpid()
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-shared", CALL_SOURCE, "-o", tmp,
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE]
     for d in (os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
@@ -76,7 +83,7 @@ def _build_call() -> None:
         print(" ".join(cmd))
         print(r.stdout + r.stderr)
         raise RuntimeError("g++ failed on %s" % CALL_SOURCE)
-    os.replace(tmp, CALL)
+    os.replace(tmp, call)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
