@@ -93,7 +93,9 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, trained_
     * ``"parts"``   pairs that turn fewer than ``beta_slow`` times in the
       ``trained_len`` tokens are slowed by ``factor``, those that turn more than
       ``beta_fast`` times are left, a linear ramp between; rope_factor is
-      0.1 ln(factor) + 1
+      0.1 ln(factor) + 1.  The ramp is linear in the turns; where it is linear
+      in the pairs' index, frequencies inside it differ: pass such a table itself
+      (the kernels take any)
     """
     if rot_dim <= 0 or rot_dim % 2:
         raise ValueError("rot_dim must be positive and even")

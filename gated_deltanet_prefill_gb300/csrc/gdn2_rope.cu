@@ -15,7 +15,7 @@
 //
 // Bound by memory: 32768 tokens of 32 + 32 heads (half of each head rotated) take
 // 176 us, 6.10 TB/s of the 6.78 that a copy reaches; the append of 34997 tokens of
-// 32 + 32 + 32 heads to pages of 16 takes 264 us, 6.52 TB/s.  The packed fp32
+// 32 + 32 + 32 heads to pages of 16 takes 262 us, 6.57 TB/s.  The packed fp32
 // instructions keep the issue slots below what the loads need.  A warp takes all
 // heads of a token when there are tokens enough to fill the GPU, and a slice of
 // them otherwise, so that a decode step is one row group per warp (128 tokens of
@@ -45,9 +45,11 @@ constexpr int kWarpsPerSm = 16;
 // Angle per position as a fraction of a turn in units of 2^-64 turns: f / (2
 // pi) * 2^64 modulo 2^64, from the double's bits (integers only: double
 // arithmetic would cost more than the rest of the token).  position * fraction
-// wraps modulo a turn by itself, so the angle of any position is exact to the
-// frequency's own rounding.  With f = M 2^(e - 63), M in [2^63, 2^64), and
-// C = 2^66 / (2 pi): f 2^64 / (2 pi) = M C 2^(e - 65).
+// wraps modulo a turn by itself, so the angle is off by no more than the fraction is,
+// times the position: less than 1.4 x 2^-64 turns per position for f <= 1 (one for the
+// bits cut off, f / pi for those of C), less than 2^-31 turns at position 2^32.
+// With f = M 2^(e - 63), M in [2^63, 2^64), and C = 2^66 / (2 pi):
+// f 2^64 / (2 pi) = M C 2^(e - 65).
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
     constexpr uint64_t C = 0xA2F9836E4E441529ull;  // floor(2^66 / (2 pi)) = floor(2^64 * 2 / pi)
     const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));

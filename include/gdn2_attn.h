@@ -92,9 +92,10 @@ GDN2_API gdn2_status gdn2_attn_dims_init(gdn2_attn_dims *dims, int64_t T_tot, in
  *     (x_a, x_b) <- rope_factor (x_a cos - x_b sin, x_a sin + x_b cos),
  *                   angle = position * inv_freq[i], for each pair i
  *
- * and one rounding to `dtype` at the end.  The angle is reduced exactly (in
- * 64-bit fixed point) before the sine and cosine, so positions of any size
- * lose nothing.
+ * and one rounding to `dtype` at the end.  The angle is reduced in 64-bit fixed
+ * point before the sine and cosine: for frequencies up to 1 it is off by less
+ * than |position| 2^-60 radians, nothing at 16 bits for int32 positions and up
+ * to some 2^40; int64 positions far past that turn by angles that mean nothing.
  *
  *   q, q_out            both NULL: queries are left out; likewise k, k_out
  *                       (not both pairs)
