@@ -194,6 +194,16 @@ def _check_inputs(q, k, v, cu_seqlens, initial_state, **others):
         raise ValueError("initial_state must be contiguous [N, HS, K, V]")
 
 
+def _keep(stream, device, made):
+    """Memory made here belongs to the current stream: where the call runs on
+    another, it must not be handed out again before that one has passed the call."""
+    if not made or stream == torch.cuda.current_stream(device).cuda_stream:
+        return
+    s = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    for t in made:
+        t.record_stream(s)
+
+
 def chunk_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_state=None,
                    cu_seqlens=None, output_final_state=True, use_qk_l2norm=False, out=None,
                    final_state=None, workspace=None, impl="tc", stream=None, stage_events=None,
@@ -214,16 +224,20 @@ def chunk_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_state
     V = v.shape[2]
     HS = state_heads(q, v)
     N = cu_seqlens.numel() - 1
+    made = []
     if out is None:
         out = torch.empty((T, HS, V), dtype=q.dtype, device=q.device)
+        made.append(out)
     sdt = _state_dtype(initial_state, final_state, state_dtype)
     if final_state is None and output_final_state:
         final_state = torch.empty((N, HS, K, V), dtype=sdt, device=q.device)
+        made.append(final_state)
     dims = make_dims(q, k, v, g, beta, w, out, cu_seqlens, use_qk_l2norm, impl, state_v_major, sdt)
     dims.state_segments = int(state_segments)  # 0: chosen by the library
     nbytes = workspace_bytes(dims)
     if workspace is None:
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        made.append(workspace)
     if stream is None:
         stream = torch.cuda.current_stream(q.device).cuda_stream
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(w),
@@ -236,6 +250,7 @@ def chunk_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_state
         else:
             arr = (ctypes.c_void_p * len(stage_events))(*[e.cuda_event for e in stage_events])
             st = lib.gdn2_chunk_fwd_staged(*args, arr, len(stage_events))
+    _keep(stream, q.device, made)
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_chunk_fwd")
     return out, final_state
@@ -255,11 +270,14 @@ def chunk_gdn2_fwd_noalloc(q, k, v, g=None, beta=None, w=None, scale=None, initi
     V = v.shape[2]
     HS = state_heads(q, v)
     N = cu_seqlens.numel() - 1
+    made = []
     if out is None:
         out = torch.empty((T, HS, V), dtype=q.dtype, device=q.device)
+        made.append(out)
     sdt = _state_dtype(initial_state, final_state, state_dtype)
     if final_state is None and output_final_state:
         final_state = torch.empty((N, HS, K, V), dtype=sdt, device=q.device)
+        made.append(final_state)
     dims = make_dims(q, k, v, g, beta, w, out, cu_seqlens, use_qk_l2norm, impl, state_v_major, sdt)
     if stream is None:
         stream = torch.cuda.current_stream(q.device).cuda_stream
@@ -268,6 +286,7 @@ def chunk_gdn2_fwd_noalloc(q, k, v, g=None, beta=None, w=None, scale=None, initi
                                         ctypes.c_float(0.0 if scale is None else float(scale)),
                                         _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
                                         ctypes.byref(dims), stream)
+    _keep(stream, q.device, made)
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_chunk_fwd_noalloc")
     return out, final_state
@@ -287,14 +306,18 @@ def recurrent_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_s
     V = v.shape[2]
     HS = state_heads(q, v)
     N = cu_seqlens.numel() - 1
+    made = []
     if out is None:
         out = torch.empty((T, HS, V), dtype=q.dtype, device=q.device)
+        made.append(out)
     sdt = _state_dtype(initial_state, final_state, state_dtype)
     if final_state is None and output_final_state:
         final_state = torch.empty((N, HS, K, V), dtype=sdt, device=q.device)
+        made.append(final_state)
     dims = make_dims(q, k, v, g, beta, w, out, cu_seqlens, use_qk_l2norm, "tc", state_v_major, sdt)
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=q.device)
+        made.append(workspace)
     if stream is None:
         stream = torch.cuda.current_stream(q.device).cuda_stream
     with torch.cuda.device(q.device):
@@ -302,6 +325,7 @@ def recurrent_gdn2_fwd(q, k, v, g=None, beta=None, w=None, scale=None, initial_s
                                     ctypes.c_float(0.0 if scale is None else float(scale)),
                                     _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
                                     ctypes.byref(dims), _ptr(workspace), workspace.numel(), stream)
+    _keep(stream, q.device, made)
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_recurrent_fwd")
     return out, final_state
